@@ -5,4 +5,4 @@ include/ibp.h); `host_transfer_amd.ibp` is its thin ctypes binding and
 `host_transfer_amd.workloads` draws the seeded synthetic inputs.  Importing
 this package loads nothing: the library is loaded by the binding on first use.
 """
-__all__ = ["ibp", "workloads"]
+__all__ = ["ibp", "kv", "workloads"]

@@ -11,6 +11,7 @@
 
 #include "ibp.h"
 #include "ibp_internal.h"
+#include "kv.h"
 
 namespace {
 
@@ -112,6 +113,16 @@ hipError_t scratch_address(uint32_t** out) {
 }  // namespace
 
 namespace ibp {
+
+// The error text of entry points in other files (kv.h).
+int set_error(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_err, sizeof g_err, fmt, ap);
+  va_end(ap);
+  return code;
+}
+int clear_error() { return ok(); }
 
 hipError_t device_info(DeviceInfo* out) {
   int dev = 0;

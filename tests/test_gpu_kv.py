@@ -1,0 +1,519 @@
+"""The paged K/V operators on the GPU against plain 64-bit computations
+(tests/kv_case.py): placement with norm and rotation, page bounds, attention
+over the cache, page selection and attention over the selected pages, at the
+sizes, strides and masks where they can go wrong."""
+import math
+
+import pytest
+import torch
+
+from host_transfer_amd import kv
+from tests import kv_case as K
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16 = torch.float16, torch.bfloat16
+PAD = -4.25  # what rows and pages that a call must leave alone hold
+
+
+def log(msg):
+    print("[kv] " + msg, flush=True)
+
+
+def ws(nbytes):
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+
+
+def gpu_batch(c, max_q=None, max_kv=None):
+    return kv.Batch(c.q_start.cuda(), c.kv_len.cuda(), c.table.cuda(),
+                    c.max_q if max_q is None else max_q, c.max_kv if max_kv is None else max_kv)
+
+
+def run_attend(c, scale, causal=True, window=0, sel=None, max_q=None, max_kv=None):
+    k, v = c.pools()
+    cache, batch = kv.Cache(k, v), gpu_batch(c, max_q, max_kv)
+    hq = c.h * c.group
+    q = c.wide_q.cuda()[:, :hq]
+    out = torch.full((c.n, hq + 1, c.d), PAD, dtype=c.dtype, device="cuda")
+    lse = torch.full((c.n, hq), PAD, device="cuda")
+    if sel is None:
+        w = ws(kv.attend_workspace(cache, batch, c.n, hq))
+        kv.attend(cache, batch, q, out[:, :hq], scale, window=window,
+                  flags=kv.CAUSAL if causal else 0, lse=lse, workspace=w)
+    else:
+        w = ws(kv.attend_selected_workspace(cache, batch, c.n, hq, sel.shape[2]))
+        kv.attend_selected(cache, batch, q, sel.cuda(), out[:, :hq], scale, lse=lse, workspace=w)
+    torch.cuda.synchronize()
+    assert (out[:, hq] == PAD).all(), "wrote past the heads of out"
+    return out[:, :hq], lse
+
+
+# ---------------------------------------------------------------- append
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,rope,inter,norm", [
+    (8, 0, False, False), (16, 16, False, True), (64, 64, False, True), (64, 32, True, True),
+    (80, 80, False, False), (80, 48, True, True), (96, 96, False, True), (128, 128, False, True),
+    (128, 128, True, False), (128, 32, False, True), (136, 0, False, True), (192, 192, False, True),
+    (256, 256, False, True), (256, 128, True, True)])
+def test_append(dtype, d, rope, inter, norm):
+    for n, hq, h, page, head_major in ((1, 3, 1, 16, False), (37, 4, 2, 24, True), (70, 0, 5, 1, False)):
+        g = torch.Generator().manual_seed(n + d)
+        n_pages = -(-n // page) + 2
+        log(f"append {dtype} d={d} rope={rope} inter={inter} norm={norm} n={n} hq={hq} page={page}")
+        qkv = torch.randn((n, hq + 2 * h, d), generator=g).to(dtype)
+        slots = torch.randperm(n_pages * page, generator=g)[:n]
+        pos = torch.randint(0, 50, (n,), generator=g)
+        if n > 5:  # tokens that are not placed: padding, past the pool, past the table
+            slots[1], slots[2], slots[3] = -1, n_pages * page, 1 << 40
+            if rope:
+                pos[4], pos[5] = 50, -1
+        placed = (slots >= 0) & (slots < n_pages * page)
+        if rope:
+            placed &= (pos >= 0) & (pos < 50)
+        table = K.rope_table(50, rope) if rope else None
+        qn = (1 + 0.3 * torch.randn(d, generator=g)).to(dtype) if norm else None
+        kn = (1 + 0.3 * torch.randn(d, generator=g)).to(dtype) if norm else None
+        pools = [torch.full((n_pages, page, h, d), PAD, dtype=dtype, device="cuda") for _ in "kv"]
+        if head_major:
+            pools = [x.transpose(1, 2).contiguous().transpose(1, 2) for x in pools]
+        gpu = qkv.cuda()
+        q_out = torch.full((n, hq, d), PAD, dtype=dtype, device="cuda") if hq else None
+        dev = lambda t: None if t is None else t.cuda()
+        kv.append(kv.Cache(*pools), gpu[:, hq:hq + h], gpu[:, hq + h:], slots.cuda(),
+                  q=gpu[:, :hq] if hq else None, q_out=q_out, positions=dev(pos) if rope else None,
+                  rope=dev(table), flags=kv.ROPE_INTERLEAVED if inter else 0, q_norm=dev(qn),
+                  k_norm=dev(kn), eps=1e-5)
+        torch.cuda.synchronize()
+        safe = pos.clamp(0, 49)
+        want = [K.norm_rotate(qkv[:, a:b].double(), safe, table, inter, w, 1e-5)
+                for a, b, w in ((0, hq, qn), (hq, hq + h, kn))]
+        u = K.half_step(dtype)
+        # fp32: the sum of d squares, the root, three products, the rotation's two products and sum
+        rel = u + (d + 16) * K.U32
+        tiny = torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2
+        rows_k, rows_v = (x.cpu().reshape(-1, h, d) for x in pools)
+        # the rotation's output is bounded by the pair's length, not by itself
+        length = lambda x: x.abs().amax(-1, keepdim=True) * (2 if rope else 0) * 16 * K.U32
+        err = (rows_k[slots[placed]].double() - want[1][placed]).abs()
+        assert (err <= rel * want[1][placed].abs() + length(want[1][placed]) + tiny).all()
+        assert torch.equal(rows_v[slots[placed]], qkv[placed, hq + h:])
+        left = torch.ones(n_pages * page, dtype=torch.bool)
+        left[slots[placed]] = False
+        assert (rows_k[left] == PAD).all() and (rows_v[left] == PAD).all(), "touched other rows"
+        if not norm and not rope:
+            assert torch.equal(rows_k[slots[placed]], qkv[placed, hq:hq + h])
+        if hq:
+            got = q_out.cpu()
+            assert (got[~placed] == 0).all()
+            err = (got[placed].double() - want[0][placed]).abs()
+            assert (err <= rel * want[0][placed].abs() + length(want[0][placed]) + tiny).all()
+
+
+def test_append_in_place_and_broadcast():
+    """q_out = q; one key row for all tokens (stride 0); a strided page pool (K and V side by side)."""
+    n, hq, h, d, page = 19, 6, 3, 64, 8
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn((n, hq, d), generator=g).to(BF16)
+    k = torch.randn((1, h, d), generator=g).to(BF16)
+    pool = torch.full((4, 2, page, h, d), PAD, dtype=BF16, device="cuda")
+    table = K.rope_table(32, d)
+    pos = torch.arange(n)
+    slots = torch.arange(n) + 3
+    gq, gk = q.cuda(), k.cuda().expand(n, h, d)
+    log("append in place")
+    kv.append(kv.Cache(pool[:, 0], pool[:, 1]), gk, gk, slots.cuda(), q=gq, q_out=gq,
+              positions=pos.cuda(), rope=table.cuda())
+    torch.cuda.synchronize()
+    want = K.norm_rotate(q.double(), pos, table, False, None, 0)
+    lim = K.half_step(BF16) * want.abs() + 32 * K.U32 * want.abs().amax(-1, keepdim=True)
+    assert ((gq.cpu().double() - want).abs() <= lim).all()
+    wk = K.norm_rotate(k.double().expand(n, h, d), pos, table, False, None, 0)
+    rows = pool[:, 0].cpu().reshape(-1, h, d)
+    lim = K.half_step(BF16) * wk.abs() + 32 * K.U32 * wk.abs().amax(-1, keepdim=True)
+    assert ((rows[slots].double() - wk).abs() <= lim).all()
+    assert (rows[:3] == PAD).all() and (rows[n + 3:] == PAD).all()
+    assert torch.equal(pool[:, 1].cpu().reshape(-1, h, d)[slots], k.expand(n, h, d))
+
+
+# ---------------------------------------------------------------- bounds
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,h,page", [(8, 1, 1), (64, 3, 16), (80, 2, 24), (128, 8, 64), (256, 1, 7)])
+def test_page_bounds(dtype, d, h, page):
+    lens = [(1, 1), (0, 40), (5, 5), (3, page * 2 + 1), (40, 129), (1, page * 3), (2, 0), (1, 2 * page)]
+    c = K.Case(lens, dtype=dtype, h=h, group=1, d=d, page=page, fill=math.nan)
+    c.k[int(c.table[7, 1]), min(1, page - 1), 0, 2] = math.nan
+    c.k[int(c.table[5, 2]), 0, 0, 1] = math.inf
+    c.table[0, 0] = c.n_pages  # a page that is not there
+    log(f"bounds {dtype} d={d} h={h} page={page}")
+    k, v = c.pools()
+    bounds = torch.full((c.n_pages, h, 2, d), PAD, dtype=dtype, device="cuda")
+    kv.page_bounds(kv.Cache(k, v), gpu_batch(c), bounds)
+    torch.cuda.synchronize()
+    got = bounds.cpu()
+    want = K.page_bounds(c)
+    for i in range(c.n_pages):
+        if i in want:
+            for side in (0, 1):
+                a, b = got[i, :, side], want[i][side]
+                assert ((a == b) | (torch.isnan(a) & torch.isnan(b))).all(), (i, side)
+        else:
+            assert (got[i] == PAD).all(), "touched another page"
+
+
+# ---------------------------------------------------------------- attention
+
+LENS = [(1, 1), (3, 3), (0, 0), (17, 64), (1, 65), (2, 200), (0, 31), (130, 300), (66, 66)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,h,group,page", [(8, 1, 1, 16), (40, 2, 3, 8), (64, 2, 4, 16), (80, 1, 2, 24),
+                                            (96, 2, 1, 1), (128, 2, 8, 16), (128, 1, 5, 64),
+                                            (136, 1, 2, 16), (192, 2, 2, 32), (256, 1, 20, 16)])
+def test_attend(dtype, d, h, group, page):
+    c = K.Case(LENS, dtype=dtype, h=h, group=group, d=d, page=page, fill=math.nan, tail_rows=3,
+               head_major=page == 16)
+    scale = 1 / math.sqrt(d)
+    for causal, window in ((True, 0), (True, 1), (True, 50), (False, 0)):
+        log(f"attend {dtype} d={d} h={h} group={group} page={page} causal={causal} window={window}")
+        out, lse = run_attend(c, scale, causal, window)
+        K.check_attention(c, out, lse, K.attention(c, scale, causal=causal, window=window),
+                          f"causal={causal} window={window}")
+        assert (out[c.n - 3:] == PAD).all() and (lse[c.n - 3:] == PAD).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,h,group,page", [(64, 2, 1, 16), (80, 1, 4, 24), (96, 2, 2, 16),
+                                            (128, 2, 4, 16), (128, 1, 16, 1), (192, 1, 17, 64),
+                                            (256, 1, 3, 32)])
+def test_attend_single_tokens(dtype, d, h, group, page):
+    """One new token a sequence, from one key to several splits of the keys."""
+    lens = [(1, n) for n in (1, 2, 15, 16, 17, 31, 64, 65, 127, 257, 1000, 2049)] + [(0, 0), (1, 700)]
+    c = K.Case(lens, dtype=dtype, h=h, group=group, d=d, page=page, fill=math.nan, tail_rows=1)
+    scale = 0.7 / math.sqrt(d)
+    for causal, window, max_kv in ((True, 0, None), (True, 33, None), (False, 0, None),
+                                   (True, 0, 20000)):
+        if max_kv:
+            c.table = torch.cat([c.table, torch.full((len(lens), 20000 // page + 1), 1 << 30,
+                                                     dtype=torch.int32)], 1)
+        log(f"single tokens {dtype} d={d} group={group} page={page} window={window} max_kv={max_kv}")
+        out, lse = run_attend(c, scale, causal, window, max_kv=max_kv)
+        K.check_attention(c, out, lse, K.attention(c, scale, causal=causal, window=window))
+        assert (out[c.n - 1:] == PAD).all() and (lse[c.n - 1:] == PAD).all()
+
+
+@pytest.mark.parametrize("q", [1, 2, 5, 40, 200])
+def test_attend_bad_pages_and_lengths(q):
+    """Pages that are not there (ids of every wrong kind), lengths past the bounds given, rows
+    at positions before the first token."""
+    lens = [(q, 400), (q, 170), (q, q - 1 if q < 3 else q // 2), (q, 250)]
+    c = K.Case(lens, d=64, h=2, group=2, page=16, fill=math.nan, seed=q)
+    for s, p, bad in ((0, 0, -1), (0, 7, c.n_pages), (0, 24, 1 << 30), (1, 3, -(1 << 31)),
+                      (3, 15, -5), (3, 14, -5), (3, 13, c.n_pages + 7)):
+        c.table[s, p] = bad
+    log(f"bad pages q={q}")
+    out, lse = run_attend(c, 0.125)
+    K.check_attention(c, out, lse, K.attention(c, 0.125), f"q={q}")
+    # a sequence whose pages are all missing
+    c.table[0] = -1
+    out, lse = run_attend(c, 0.125)
+    K.check_attention(c, out, lse, K.attention(c, 0.125), f"q={q}: no page")
+    # tokens past max_kv are not read, new tokens past max_q are left as they were
+    c = K.Case([(q, 400), (q, 170)], d=64, h=2, group=2, page=16, fill=math.nan, seed=q)
+    out, lse = run_attend(c, 0.125, causal=False, max_kv=300)
+    full = c.lens
+    ref_c = K.Case([(q, 400), (q, 170)], d=64, h=2, group=2, page=16, fill=math.nan, seed=q)
+    ref_c.table[0, 19:] = -1
+    ref_c.table[0, 18] = c.table[0, 18]
+    cut = ref_c.keys
+    ref_c.keys = lambda s, upto=None: cut(s, 300)
+    K.check_attention(c, out, lse, K.attention(ref_c, 0.125, causal=False), f"q={q}: max_kv")
+    assert full == c.lens
+    if q > 1:
+        out, lse = run_attend(c, 0.125, max_q=q - 1)
+        assert (out[q - 1] == PAD).all() and (out[2 * q - 1] == PAD).all()
+        want = K.attention(c, 0.125)
+        want[4][[q - 1, 2 * q - 1]] = False
+        K.check_attention(c, out, lse, want, f"q={q}: max_q")
+
+
+@pytest.mark.parametrize("q", [1, 3, 40, 150])
+def test_attend_values_out_of_range(q):
+    """NaN and infinite keys and values: a row that sees one carries it, another does not."""
+    lens = [(q, 190), (q, 333)]
+    for kind, val in (("v", math.nan), ("v", math.inf), ("v", -math.inf), ("k", math.nan)):
+        c = K.Case(lens, dtype=BF16, d=64, h=2, group=2, page=16, seed=3)
+        for s, (_, n) in enumerate(lens):
+            for j, ch in ((n - 1, 5), (n - 1 - q // 2, 6), (n - q // 2 - 40, 7)):
+                j = max(0, j)
+                x = c.k if kind == "k" else c.v
+                if kind == "k" and j < n - 1 - q // 2:
+                    continue  # a NaN score for every row
+                x[int(c.table[s, j // 16]), j % 16, 1, ch] = val
+        log(f"out of range {kind}={val} q={q}")
+        for window in (0, 20):
+            out, lse = run_attend(c, 0.125, window=window)
+            K.check_attention(c, out, lse, K.attention(c, 0.125, window=window), f"{kind}={val}")
+
+
+def test_attend_large_scores():
+    """Scores far apart (a softmax of one key), and all equal."""
+    for dtype in (F16, BF16):
+        for scale in (0.0, 30.0, -5.0):
+            c = K.Case([(1, 300), (33, 140), (70, 500)], dtype=dtype, d=64, h=1, group=2, page=16)
+            log(f"large scores {dtype} {scale}")
+            out, lse = run_attend(c, scale)
+            K.check_attention(c, out, lse, K.attention(c, scale), f"scale={scale}")
+    # rising scores: every tile has a new maximum
+    c = K.Case([(1, 700), (64, 700)], dtype=F16, d=64, h=1, group=1, page=16)
+    c.q[:] = 1.0
+    for s in range(2):
+        for j in range(700):
+            c.k[int(c.table[s, j // 16]), j % 16] = (j - 350) / 16.0
+    log("rising scores")
+    out, lse = run_attend(c, 0.25)
+    K.check_attention(c, out, lse, K.attention(c, 0.25), "rising")
+
+
+# ---------------------------------------------------------------- selection
+
+SEL_LENS = [(1, 1), (1, 500), (0, 0), (7, 333), (1, 16), (3, 17), (1, 999), (2, 1), (40, 260)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,h,group,page,first,last,n_select", [
+    (64, 2, 1, 16, 0, 1, 4), (128, 2, 4, 16, 1, 2, 8), (80, 1, 3, 8, 1, 1, 2), (256, 1, 8, 16, 2, 3, 21),
+    (8, 2, 2, 32, 0, 1, 1), (96, 3, 2, 1, 4, 4, 50), (128, 1, 16, 24, 1, 1, 64)])
+def test_select_and_attend(dtype, d, h, group, page, first, last, n_select):
+    c = K.Case(SEL_LENS, dtype=dtype, d=d, h=h, group=group, page=page, fill=math.nan, tail_rows=2)
+    bounds = K.all_bounds(c)
+    log(f"select {dtype} d={d} h={h} group={group} page={page} {first}/{last}/{n_select}")
+    k, v = c.pools()
+    cache, batch = kv.Cache(k, v), gpu_batch(c)
+    sel = torch.full((c.n, h, n_select), -7, dtype=torch.int32, device="cuda")
+    q = c.wide_q.cuda()[:, :h * group]
+    kv.select(cache, batch, bounds.cuda(), q, sel, n_first=first, n_last=last,
+              workspace=ws(kv.select_workspace(cache, batch, c.n, n_select)))
+    torch.cuda.synchronize()
+    want = K.select(c, bounds, first, last, n_select)
+    assert torch.equal(sel.cpu(), want)
+    scale = 1 / math.sqrt(d)
+    out, lse = run_attend(c, scale, sel=want)
+    K.check_attention(c, out, lse, K.attention(c, scale, sel=want), "selected")
+    assert (out[c.n - 2:] == PAD).all() and (lse[c.n - 2:] == PAD).all()
+
+
+def test_select_ties_and_odd_scores():
+    """Equal scores take the lower page; NaN bounds rank first, pages without bounds last, signed
+    zeros tie."""
+    page, n_pages = 4, 300
+    c = K.Case([(1, page * n_pages)], dtype=F16, d=16, h=1, group=2, page=page, extra=0)
+    bounds = torch.zeros(c.n_pages, 1, 2, 16, dtype=F16)
+    ids = c.table[0, :n_pages].long()
+    c.q[:] = 1.0
+    bounds[ids[100:200], 0, 1] = 2.0
+    bounds[ids[50:60]] = -0.0
+    bounds[ids[250], 0, :, 3] = math.nan
+    bounds[ids[251], 0, 1, 3] = math.inf
+    bounds[ids[252], 0, :, 3] = -math.inf
+    c.table[0, 120] = -1
+    c.table[0, 130] = 1 << 20
+    k, v = c.pools()
+    for n_select in (4, 30, 103, 104, 120, 170, 297, 298, 299, 300):
+        sel = torch.full((1, 1, n_select), -7, dtype=torch.int32, device="cuda")
+        cache, batch = kv.Cache(k, v), gpu_batch(c)
+        log(f"ties {n_select}")
+        kv.select(cache, batch, bounds.cuda(), c.wide_q.cuda()[:, :2], sel, n_first=1, n_last=1,
+                  workspace=ws(kv.select_workspace(cache, batch, 1, n_select)))
+        assert torch.equal(sel.cpu(), K.select(c, bounds, 1, 1, n_select)), n_select
+
+
+def test_attend_selected_lists():
+    """Lists with repeats, pages past the sequence, gaps and nothing at all."""
+    c = K.Case([(1, 100), (3, 260), (1, 90)], d=64, h=2, group=3, page=16, fill=math.nan)
+    sel = torch.full((c.n, 2, 6), -1, dtype=torch.int32)
+    lists = [[0, 2, 2, 6, -1, -1], [1, 40, 3, 1 << 30, -1, 2], [-1] * 6, [0, 1, 2, 3, 4, 16],
+             [5, 5, 5, 5, 5, 5]]
+    for r in range(c.n):
+        sel[r, 0] = torch.tensor(lists[r])
+        sel[r, 1] = torch.tensor(lists[(r + 2) % 5])
+    # what the rule leaves of each list: in range and above the entry before it
+    pages = c.table.shape[1] - 1
+    kept = sel.clone()
+    for r in range(c.n):
+        for h in range(2):
+            for e in range(6):
+                x = int(sel[r, h, e])
+                if not 0 <= x < -(-c.max_kv // 16) or (e and x <= int(sel[r, h, e - 1])):
+                    kept[r, h, e] = -1
+    assert pages >= 17
+    log("lists")
+    out, lse = run_attend(c, 0.125, sel=sel)
+    K.check_attention(c, out, lse, K.attention(c, 0.125, sel=kept), "lists")
+
+
+# ---------------------------------------------------------------- together
+
+def test_decode_loop_with_the_compressed_store():
+    """Prompt and decode steps as a user runs them: rows appended to the paged cache, the new rows
+    compressed on write, pages fetched back from the compressed store into a second pool, and
+    attention over both pools giving the same bits; pages selected and attended; the decode step
+    captured in a graph and replayed with new lengths."""
+    from host_transfer_amd import ibp
+    h, group, d, page, n_pages, steps = 4, 2, 64, 16, 24, 5
+    hq, width = h * group, h * d
+    prompt = [37, 64, 5]
+    g = torch.Generator().manual_seed(9)
+    pools = [torch.zeros((n_pages, page, h, d), dtype=F16, device="cuda") for _ in "kv"]
+    cache = kv.Cache(*pools)
+    table = torch.full((3, 8), -1, dtype=torch.int32)
+    order = torch.randperm(n_pages, generator=g)
+    for s in range(3):
+        table[s] = order[s * 8:(s + 1) * 8]
+    rope = K.rope_table(128, d)
+    kn, qn = (1 + 0.2 * torch.randn(2, d, generator=g)).to(F16)
+    d_table, d_rope, d_kn, d_qn = table.cuda(), rope.cuda(), kn.cuda(), qn.cuda()
+    # IBP metadata over a sample of rows of that shape
+    sample = torch.randn((256, width), generator=g).to(F16).cuda()
+    B, C, rows_n = 2 * width, 256, n_pages * page
+    mask, bitval = (torch.zeros(B // 4, dtype=torch.int32, device="cuda") for _ in range(2))
+    counts = torch.zeros(8 * B, dtype=torch.int32, device="cuda")
+    ibp.build_metadata(sample, B, None, 256, B, 0.99, mask, bitval, counts)
+    store = ibp.HostBuffer(rows_n * B)
+    part = torch.zeros((rows_n * (B // C) + 31) // 32, dtype=torch.int32, device="cuda")
+
+    def slots_of(s, pos):
+        return int(table[s, pos // page]) * page + pos % page
+
+    def feed(lens, new):
+        """Appends `new[s]` tokens of each sequence (all but the last `new` are there)."""
+        n = sum(new)
+        qkv = torch.randn((n, hq + 2 * h, d), generator=g).to(F16).cuda()
+        pos = [kv_n - q + i for kv_n, q in zip(lens, new) for i in range(q)]
+        seq = [s for s, q in enumerate(new) for _ in range(q)]
+        slots = torch.tensor([slots_of(s, p) for s, p in zip(seq, pos)])
+        q_out = torch.empty((n, hq, d), dtype=F16, device="cuda")
+        kv.append(cache, qkv[:, hq:hq + h], qkv[:, hq + h:], slots.cuda(), q=qkv[:, :hq], q_out=q_out,
+                  positions=torch.tensor(pos).cuda(), rope=d_rope, q_norm=d_qn, k_norm=d_kn)
+        return q_out, slots
+
+    def batch_of(lens, new, max_q, max_kv):
+        start = torch.tensor([0] + new).cumsum(0).int().cuda()
+        return kv.Batch(start, torch.tensor(lens, dtype=torch.int32).cuda(), d_table, max_q, max_kv)
+
+    def attend(cache_, b, q):
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:2], device="cuda")
+        kv.attend(cache_, b, q, out, 0.125, lse=lse,
+                  workspace=ws(kv.attend_workspace(cache_, b, q.shape[0], hq)))
+        return out, lse
+
+    bounds = torch.zeros((n_pages, h, 2, d), dtype=F16, device="cuda")
+    lens, new = list(prompt), list(prompt)
+    for step in range(steps):
+        log(f"decode loop step {step}: {lens}")
+        q, slots = feed(lens, new)
+        b = batch_of(lens, new, max(new), 128)
+        kv.page_bounds(cache, b, bounds)
+        out, lse = attend(cache, b, q)
+        # the new rows of K (pool 0) into the compressed store, each a segment of one row
+        kp = pools[0].view(rows_n, width)
+        for lo in range(0, len(slots), 200):
+            part_slots = slots[lo:lo + 200].tolist()
+            ibp.compress_segments(kp, B, part_slots, part_slots, [1] * len(part_slots), rows_n, B, C,
+                                  mask.repeat(len(part_slots)), bitval.repeat(len(part_slots)), store,
+                                  B, part, None)
+        # all pages back from the store into another pool, in another order of pages
+        perm = torch.randperm(n_pages, generator=g)
+        ids = (perm[:, None] * page + torch.arange(page)).reshape(-1).cuda()
+        k2 = torch.zeros_like(pools[0])
+        ibp.gather_decompress(store, rows_n * B, B, None, part, rows_n, ids, rows_n, B, C, mask,
+                              bitval, k2)
+        v2 = pools[1][perm.cuda()].contiguous()
+        inv = torch.empty_like(perm)
+        inv[perm] = torch.arange(n_pages)
+        b2 = kv.Batch(b._keep[0], b._keep[1], inv[table.long()].int().cuda(), max(new), 128)
+        out2, lse2 = attend(kv.Cache(k2, v2), b2, q)
+        torch.cuda.synchronize()
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+        # the same from the formulas
+        c = K.Case([(a, l) for a, l in zip(new, lens)], dtype=F16, h=h, group=group, d=d, page=page)
+        c.k, c.v, c.table, c.n_pages = pools[0].cpu(), pools[1].cpu(), table, n_pages
+        c.q, c.n = q.cpu(), q.shape[0]
+        K.check_attention(c, out, lse, K.attention(c, 0.125), f"step {step}")
+        assert torch.equal(bounds.cpu()[table[0, (lens[0] - 1) // page]],
+                           K.all_bounds(c)[table[0, (lens[0] - 1) // page]])
+        sel = torch.empty((c.n, h, 3), dtype=torch.int32, device="cuda")
+        kv.select(cache, b, bounds, q, sel, n_first=1, n_last=1,
+                  workspace=ws(kv.select_workspace(cache, b, c.n, 3)))
+        want = K.select(c, K.all_bounds(c), 1, 1, 3)
+        assert torch.equal(sel.cpu(), want)
+        o3, l3 = torch.empty_like(q), torch.empty_like(lse)
+        kv.attend_selected(cache, b, q, sel, o3, 0.125, lse=l3,
+                           workspace=ws(kv.attend_selected_workspace(cache, b, c.n, hq, 3)))
+        K.check_attention(c, o3, l3, K.attention(c, 0.125, sel=want), f"selected, step {step}")
+        lens, new = [x + 1 for x in lens], [1, 1, 1]
+    store.free()
+
+
+def test_graph_replay_and_streams():
+    """A decode step (append, bounds, attend, select, attend_selected) captured once and replayed
+    with other inputs in the same buffers, eager work between; and attention on two streams at
+    the same time.  The same bits as eager calls every time."""
+    c = K.Case([(1, 900), (1, 300), (1, 1)], dtype=BF16, d=128, h=2, group=4, page=16)
+    k, v = c.pools()
+    cache = kv.Cache(k, v)
+    hq, n = 8, 3
+    batch = gpu_batch(c, max_kv=928)
+    q = c.wide_q.cuda()[:, :hq].contiguous()
+    rows = torch.randn((n, 2, 2, 128), device="cuda").to(BF16)
+    slots = torch.tensor([5, 60, 100], device="cuda")
+    bounds = K.all_bounds(c).cuda()
+    w1 = ws(kv.attend_workspace(cache, batch, n, hq))
+    w2 = ws(max(kv.select_workspace(cache, batch, n, 10),
+                kv.attend_selected_workspace(cache, batch, n, hq, 10)))
+
+    def step(out, lse, sel, out2):
+        kv.append(cache, rows[:, 0], rows[:, 1], slots)
+        kv.page_bounds(cache, batch, bounds)
+        kv.attend(cache, batch, q, out, 0.1, lse=lse, workspace=w1)
+        kv.select(cache, batch, bounds, q, sel, n_first=1, n_last=2, workspace=w2)
+        kv.attend_selected(cache, batch, q, sel, out2, 0.1, workspace=w2)
+
+    def buffers():
+        return (torch.zeros((n, hq, 128), dtype=BF16, device="cuda"), torch.zeros((n, hq), device="cuda"),
+                torch.zeros((n, 2, 10), dtype=torch.int32, device="cuda"),
+                torch.zeros((n, hq, 128), dtype=BF16, device="cuda"))
+    got, want = buffers(), buffers()
+    step(*got)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    log("capture")
+    with torch.cuda.graph(graph):
+        step(*got)
+    for rep in range(4):
+        q.copy_(torch.randn_like(q))
+        rows.copy_(torch.randn_like(rows))
+        batch._keep[1].copy_(torch.tensor([900 - 100 * rep, 300 - 77 * rep, 1 + rep]))
+        step(*want)
+        torch.cuda.synchronize()
+        for t in got:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), rep
+        c.k, c.v, c.q = k.cpu(), v.cpu(), q.cpu()
+        c.lens = [(1, x) for x in batch._keep[1].tolist()]
+        K.check_attention(c, got[0], got[1], K.attention(c, 0.1), f"replay {rep}")
+    # two streams, each with its workspace
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(want[0]) for _ in range(8)]
+    works = [ws(w1.numel()) for _ in streams]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        kv.attend(cache, batch, q, o, 0.1, workspace=works[i % 2], stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want[0])
