@@ -1,6 +1,6 @@
 // kv_attend.hip -- attention over a paged cache, whole or over selected pages.
 #include "ibp_device.h"
-#include "kv.h"
+#include "kv_mfma.h"
 
 namespace ibp {
 namespace kv {
@@ -101,28 +101,67 @@ __global__ __launch_bounds__(256) void k_kv_attend(Cache cache, Batch b, Rows q,
 
 }  // namespace
 
-hipError_t attend_workspace(const Cache&, const Batch&, uint32_t, uint32_t, uint64_t* bytes) {
-  *bytes = 0;
-  return hipSuccess;
+namespace {
+
+hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
+                     AttendPlan* p) {
+  DeviceInfo di;
+  hipError_t e = device_info(&di);
+  if (e != hipSuccess) return e;
+  const uint32_t group = n_q_heads / c.n_heads;
+  const uint64_t rows = (uint64_t)(n_select ? 1 : b.max_q) * group;
+  p->few = n_select || rows <= 16;
+  p->row_tiles = (uint32_t)((rows + 15) / 16);
+  const uint64_t base = (uint64_t)(n_select ? b.n_rows : b.n_seqs) * p->row_tiles * c.n_heads;
+  const uint64_t keys = n_select ? (uint64_t)n_select * c.page.d : b.max_kv;
+  const uint64_t want = (uint64_t)di.cus * 4;
+  uint64_t splits = base ? (want + base - 1) / base : 1;
+  if (splits > keys / 256) splits = keys / 256;
+  p->splits = splits < 1 ? 1 : (uint32_t)splits;
+  p->blocks = base * p->splits;
+  if (!p->few) p->splits = 1;
+  return p->blocks > 0x7FFFFFFFull ? hipErrorInvalidConfiguration : hipSuccess;
+}
+
+// The workspace: [unit][split][head_dim] floats, then [unit][split] (max, sum).
+uint64_t partial_bytes(const Cache& c, const Batch& b, uint32_t n_q_heads, const AttendPlan& p) {
+  if (p.splits == 1) return 0;
+  return (uint64_t)b.n_rows * n_q_heads * p.splits * (c.head_dim + 2) * 4;
+}
+
+}  // namespace
+
+hipError_t attend_workspace(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
+                            uint64_t* bytes) {
+  AttendPlan p;
+  hipError_t e = make_plan(c, b, n_q_heads, n_select, &p);
+  if (e == hipSuccess) *bytes = partial_bytes(c, b, n_q_heads, p);
+  return e;
 }
 
 hipError_t launch_attend(const Cache& c, uint32_t dtype, const Batch& b, const Rows& q,
                          const Rows& out, const int32_t* sel, uint32_t n_select, float scale,
                          uint32_t window, bool causal, float* lse, void* workspace,
                          hipStream_t s) {
-  (void)workspace;
-  const uint64_t blocks = ((uint64_t)b.n_rows * q.n_heads + 3) / 4;
-  if (blocks == 0 || b.n_seqs == 0) return hipSuccess;
-#define IBP_KV_ATTEND(T, SEL)                                                                   \
-  hipLaunchKernelGGL((k_kv_attend<T, SEL>), dim3((uint32_t)blocks), dim3(256), 0, s, c, b, q, out, \
-                     sel, n_select, scale, window, causal, lse)
-  if (dtype == IBP_KV_F16) {
-    if (sel) IBP_KV_ATTEND(_Float16, true);
-    else IBP_KV_ATTEND(_Float16, false);
-  } else {
-    if (sel) IBP_KV_ATTEND(__bf16, true);
-    else IBP_KV_ATTEND(__bf16, false);
+  AttendPlan p;
+  hipError_t e = make_plan(c, b, q.n_heads, n_select, &p);
+  if (e != hipSuccess) return e;
+  Partial part;
+  part.splits = p.splits;
+  part.head_dim = c.head_dim;
+  part.o = (float*)workspace;
+  part.ms = (float2*)(part.o + (uint64_t)b.n_rows * q.n_heads * p.splits * c.head_dim);
+  if (p.few) {
+    e = launch_decode(p, c, dtype, b, q, out, sel, n_select, scale, window, causal, lse, part, s);
+    if (e != hipSuccess || p.splits == 1) return e;
+    return launch_join(dtype, b, out, part, lse, s);
   }
+  const uint64_t blocks = ((uint64_t)b.n_rows * q.n_heads + 3) / 4;
+#define IBP_KV_ATTEND(T)                                                                           \
+  hipLaunchKernelGGL((k_kv_attend<T, false>), dim3((uint32_t)blocks), dim3(256), 0, s, c, b, q, out, \
+                     sel, n_select, scale, window, causal, lse)
+  if (dtype == IBP_KV_F16) IBP_KV_ATTEND(_Float16);
+  else IBP_KV_ATTEND(__bf16);
 #undef IBP_KV_ATTEND
   return hipGetLastError();
 }

@@ -1,0 +1,419 @@
+// kv_decode.hip -- attention of few rows that share their keys: one new token
+// (or a few) of a sequence with the query heads of one key head, over the
+// whole cache or over the row's selected pages.
+#include <algorithm>
+
+#include "ibp_device.h"
+#include "kv_mfma.h"
+
+namespace ibp {
+namespace kv {
+
+namespace {
+
+constexpr int kTile = 32;                // keys of a wave's step
+constexpr int kWaves = 4;
+constexpr int kBlockKeys = kTile * kWaves;
+
+// A workgroup per (up to 16 rows that share a key head, split of their keys).
+// Its four waves take 32 keys at a time, in turn, each with a running
+// maximum and sum of its own; nothing is shared until the end, so no wave waits
+// for another.
+//
+// Bound by the reading of K and V: 4 * D bytes a key against 4 * D * 16
+// operations of the matrix cores, 1/10 of their rate at the rate of HBM, so
+// that empty columns (a group smaller than 16 rows) cost nothing.  A lane
+// reads the same 16 B pieces of a K and of a V row (key l%16, pieces l/16 + 4i): the
+// page lookup of a lane serves both.  K goes from the registers into the
+// first product as it is; V passes through LDS (its wave's own part), where
+// the transposed read gives the second product's operand.  LDS rows are padded by
+// 32 B: the eight rows that half a wave reads then lie in eight different 32 B
+// windows of the banks for every head_dim that is a multiple of 32.
+template <typename T, int DP, bool kSelected>
+__global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q, Rows out,
+                                                   const int32_t* __restrict__ sel,
+                                                   uint32_t n_select, float scale_log2,
+                                                   uint32_t window, bool causal,
+                                                   uint32_t row_tiles, Partial part,
+                                                   float* __restrict__ lse) {
+  constexpr int KS = DP / 32;   // products of the scores; 16 B pieces of a lane and row
+  constexpr int DT = DP / 16;   // tiles of the output
+  constexpr int LD = DP + 16;   // LDS row, elements
+  constexpr int WORDS = kTile * LD / 2;  // of a wave; 16 rows of DP floats fit
+  static_assert(16 * DP <= WORDS, "the end's exchange fits the V tiles");
+  __shared__ __align__(16) uint32_t s_v[kWaves][WORDS];
+  __shared__ float s_m[kWaves][16], s_z[kWaves][16];
+
+  const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
+  const uint32_t col = lane % 16, quarter = lane / 16;
+  const uint32_t group = q.n_heads / cache.n_heads;
+  const uint32_t hd = cache.head_dim;
+
+  // block -> (sequence or row, row tile, split, key head), heads innermost: the
+  // heads of a token lie side by side in memory
+  uint32_t u = blockIdx.x;
+  const uint32_t kh = u % cache.n_heads;
+  u /= cache.n_heads;
+  const uint32_t split = u % part.splits;
+  u /= part.splits;
+  const uint32_t tile = u % row_tiles;
+  u /= row_tiles;
+
+  int32_t s = (int32_t)u, i0 = 0;
+  if (kSelected) {
+    s = seq_of_row(b, (int32_t)u);
+    if (s < 0) return;
+  }
+  const Seq sq = load_seq(b, (uint32_t)s);
+  if (kSelected) {
+    i0 = (int32_t)u - sq.row0;
+    if (i0 < 0 || i0 >= sq.q_len) return;
+  }
+  // rows of this tile: m = i * group + g, [m0, m1)
+  const uint32_t n_m = (kSelected ? 1u : (uint32_t)max(sq.q_len, 0)) * group;
+  const uint32_t m0 = tile * 16;
+  if (m0 >= n_m) return;
+  const uint32_t m1 = min(m0 + 16, n_m);
+  const bool have = m0 + col < m1;
+  const uint32_t m = have ? m0 + col : m1 - 1;
+  const int32_t i = i0 + (int32_t)(m / group);
+  const uint32_t head = kh * group + m % group;
+  const uint32_t row = (uint32_t)(sq.row0 + i);
+
+  // keys that this lane's row sees, [lo, hi), and those that any row of the tile sees
+  const int32_t pos = max(sq.first + i, -1);
+  const int32_t pos_a = max(sq.first + i0 + (int32_t)(m0 / group), -1);
+  const int32_t pos_e = max(sq.first + i0 + (int32_t)((m1 - 1) / group), -1);
+  const int32_t w = (int32_t)window;
+  const int32_t lo = w ? max(pos - w + 1, 0) : 0;
+  const int32_t hi = causal ? min(pos + 1, sq.n_keys) : sq.n_keys;
+  const int32_t lo_a = w ? max(pos_a - w + 1, 0) : 0;   // least lo
+  const int32_t lo_e = w ? max(pos_e - w + 1, 0) : 0;   // greatest
+  const int32_t hi_a = causal ? min(pos_a + 1, sq.n_keys) : sq.n_keys;  // least hi
+  const int32_t hi_e = causal ? min(pos_e + 1, sq.n_keys) : sq.n_keys;  // greatest
+
+  // the split's keys, whole tiles of the workgroup (virtual keys where pages are listed)
+  const int32_t from = kSelected ? 0 : lo_a / kBlockKeys * kBlockKeys;
+  const int32_t to = kSelected ? (int32_t)(n_select * cache.page.d) : hi_e;
+  const int32_t tiles = max(to - from + kBlockKeys - 1, 0) / kBlockKeys;
+  const int32_t per = (tiles + (int32_t)part.splits - 1) / (int32_t)part.splits;
+  const int32_t begin = from + min((int32_t)split * per, tiles) * kBlockKeys;
+  const int32_t end = min(from + min(((int32_t)split + 1) * per, tiles) * kBlockKeys, to);
+
+  const T* qp = (const T*)q.p + row * q.token_stride + (uint64_t)head * q.head_stride;
+  const T* zeros = (const T*)zero_row;
+  V8<T> qf[KS];
+#pragma unroll
+  for (int k = 0; k < KS; ++k) {
+    const uint32_t c = (k * 4 + quarter) * 8;
+    qf[k] = load_row8(have && c < hd ? qp + c : zeros);
+  }
+
+  f32x4 o[DT];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float top = -INFINITY, z = 0.f;
+
+  const int32_t* table = b.table + (uint64_t)s * b.table_stride;
+  const int32_t* list = kSelected ? sel + ((uint64_t)row * cache.n_heads + kh) * n_select : nullptr;
+  const T* kbase = (const T*)cache.k + (uint64_t)kh * cache.head_stride;
+  const T* vbase = (const T*)cache.v + (uint64_t)kh * cache.head_stride;
+  T* sv = (T*)s_v[wave];
+
+  for (int32_t t0 = begin + (int32_t)wave * kTile; t0 < end; t0 += kBlockKeys) {
+    // this lane's two keys: t0 + col and t0 + 16 + col
+    V8<T> kf[2][KS], vf[2][KS];
+    uint32_t there[2];  // bit c: key c of the 16 can be seen by a row of the tile
+    bool plain = true;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      int32_t j = t0 + a * 16 + (int32_t)col;
+      bool see = j < end;
+      if (kSelected) {
+        int32_t pg = -1;
+        uint32_t e = 0;
+        if (see) {
+          e = cache.page.div((uint32_t)j);
+          pg = list[e];
+          if (e > 0 && list[e - 1] >= pg) pg = -1;
+        }
+        see = pg >= 0 && (uint32_t)pg < b.max_pages;
+        j = see ? pg * (int32_t)cache.page.d + (j - (int32_t)(e * cache.page.d)) : 0;
+      }
+      see = see && j >= lo_a && j < hi_e;
+      int32_t id = -1;
+      uint32_t page = 0;
+      if (see) {
+        page = cache.page.div((uint32_t)j);
+        id = table[page];
+      }
+      see = id >= 0 && (uint32_t)id < cache.n_pages;
+      const uint64_t at = (uint64_t)(uint32_t)id * cache.page_stride +
+                          (uint64_t)((uint32_t)j - page * cache.page.d) * cache.token_stride;
+      const T* kp = see ? kbase + at : zeros;
+      const T* vp = see ? vbase + at : zeros;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t c = (k * 4 + quarter) * 8;
+        kf[a][k] = load_row8(c < hd ? kp + c : zeros);
+      }
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t c = (k * 4 + quarter) * 8;
+        vf[a][k] = load_row8(c < hd ? vp + c : zeros);
+      }
+      there[a] = (uint32_t)__ballot(see) & 0xFFFFu;
+      plain = plain && there[a] == 0xFFFFu;
+    }
+    // every row sees every key of the tile?  (in lists, one row: `see` said all of it)
+    if (!kSelected) plain = plain && t0 >= lo_e && t0 + kTile <= hi_a;
+
+    f32x4 sc[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      sc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) sc[a] = mfma16(kf[a][k], qf[k], sc[a]);
+    }
+    // V to LDS, row = key of the tile
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+        *(V8<T>*)(sv + (a * 16 + col) * LD + (k * 4 + quarter) * 8) = vf[a][k];
+
+    // lane's scores: keys t0 + 16 a + 4 quarter + r of its column's row
+    float x[8];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[a * 4 + r] = sc[a][r] * scale_log2;
+    if (!plain) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t kk = 4 * quarter + r;
+          bool see = (there[a] >> kk) & 1u;
+          if (!kSelected) {
+            const int32_t j = t0 + a * 16 + (int32_t)kk;
+            see = see && j >= lo && j < hi;
+          }
+          if (!see) x[a * 4 + r] = -INFINITY;
+        }
+    }
+    float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                       fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    most = max_half(max_quarter(most));
+    if (__any(most > top)) {
+      const float next = fmaxf(top, most);
+      const float keep = exp2_raw(top - (next == -INFINITY ? 0.f : next));
+      z *= keep;
+#pragma unroll
+      for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[t][r] *= keep;
+      top = next;
+    }
+    const float base = top == -INFINITY ? 0.f : top;
+    V8<T> p;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = exp2_raw(x[e] - base);
+      z += y;
+      p[e] = (T)y;  // <= 1: half a step of the dtype, relative, as the output's own rounding
+    }
+    wave_sync();
+    if (!kSelected && !plain) {
+      // A key that some rows see and others do not may hold an infinity or a
+      // NaN: times the others' weight of zero it would reach them too.  Such
+      // values are added to the rows that see them here, and are zeros in LDS.
+      bool odd[2];
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int32_t j = t0 + a * 16 + (int32_t)col;
+        odd[a] = false;
+        if (j < lo_e || j >= hi_a)
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) odd[a] |= !isfinite((float)vf[a][k][e]);
+      }
+      const uint64_t any[2] = {__ballot(odd[0]), __ballot(odd[1])};
+      if (any[0] | any[1]) {
+        for (uint32_t kk = 0; kk < kTile; ++kk) {
+          const uint64_t who = any[kk / 16];
+          if (!(((who | (who >> 16) | (who >> 32) | (who >> 48)) >> (kk % 16)) & 1u)) continue;
+          const int32_t j = t0 + (int32_t)kk;
+          const bool see = j >= lo && j < hi;
+#pragma unroll
+          for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float v = to_f32(sv[kk * LD + t * 16 + quarter * 4 + r]);
+              if (see && !isfinite(v)) o[t][r] += v;
+            }
+        }
+        wave_sync();
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+          if (odd[a])
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (!isfinite((float)vf[a][k][e]))
+                  sv[(a * 16 + col) * LD + (k * 4 + quarter) * 8 + e] = (T)0.f;
+        wave_sync();
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < DT; ++t) {
+      const T* at = sv + (4 * quarter + col / 4) * LD + t * 16 + 4 * (col % 4);
+      o[t] = mfma16(join<T>(read_tr(at), read_tr(at + 16 * LD)), p, o[t]);
+    }
+    wave_sync();
+  }
+
+  // the four waves' results together: rows of DP floats in the V tiles
+  z = sum_half(sum_quarter(z));
+  float* so = (float*)s_v[wave];
+#pragma unroll
+  for (int t = 0; t < DT; ++t) *(f32x4*)(so + col * DP + t * 16 + quarter * 4) = o[t];
+  if (quarter == 0) {
+    s_m[wave][col] = top;
+    s_z[wave][col] = z;
+  }
+  __syncthreads();
+  // 16 threads a row
+  const uint32_t r = threadIdx.x / 16;
+  if (m0 + r >= m1) return;
+  float mm = s_m[0][r];
+#pragma unroll
+  for (int a = 1; a < kWaves; ++a) mm = fmaxf(mm, s_m[a][r]);
+  float f[kWaves], zz = 0.f;
+#pragma unroll
+  for (int a = 0; a < kWaves; ++a) {
+    f[a] = exp2_raw(s_m[a][r] - (mm == -INFINITY ? 0.f : mm));
+    zz += f[a] * s_z[a][r];
+  }
+  const uint32_t rm = m0 + r;
+  const uint32_t rrow = (uint32_t)(sq.row0 + i0) + rm / group, rhead = kh * group + rm % group;
+  const uint64_t unit = (uint64_t)rrow * q.n_heads + rhead;
+  const bool whole = part.splits == 1;
+  const float inv = whole ? (zz == 0.f ? 0.f : 1.f / zz) : 1.f;
+  T* op = (T*)out.p + rrow * out.token_stride + (uint64_t)rhead * out.head_stride;
+  for (uint32_t c = threadIdx.x % 16; c < hd / 8; c += 16) {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = 0.f;
+#pragma unroll
+      for (int a = 0; a < kWaves; ++a) y[e] += f[a] * ((const float*)s_v[a])[r * DP + c * 8 + e];
+      y[e] *= inv;
+    }
+    if (whole) {
+      V8<T> v;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (T)y[e];
+      *(V8<T>*)(op + c * 8) = v;
+    } else {
+      float* to_ = part.row(unit, split) + c * 8;
+      *(f32x4*)to_ = f32x4{y[0], y[1], y[2], y[3]};
+      *(f32x4*)(to_ + 4) = f32x4{y[4], y[5], y[6], y[7]};
+    }
+  }
+  if (threadIdx.x % 16 == 0) {
+    if (!whole) part.ms[unit * part.splits + split] = make_float2(mm, zz);
+    else if (lse) lse[unit] = zz == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(zz)) * kLn2;
+  }
+}
+
+// The splits of a row together: a wave per (row, head), 16, 32 or 64 lanes (four
+// channels each) a split, the splits in turn.
+template <typename T>
+__global__ __launch_bounds__(256) void k_kv_join(Batch b, Rows out, Partial part, uint32_t lanes,
+                                                 float* __restrict__ lse) {
+  const uint32_t lane = threadIdx.x % kWave;
+  const uint64_t unit = (uint64_t)blockIdx.x * 4 + threadIdx.x / kWave;
+  if (unit >= (uint64_t)b.n_rows * out.n_heads) return;
+  const uint32_t row = (uint32_t)(unit / out.n_heads), head = (uint32_t)(unit % out.n_heads);
+  const int32_t s = seq_of_row(b, (int32_t)row);
+  if (s < 0) return;
+  const float2* ms = part.ms + unit * part.splits;
+  float mm = -INFINITY;
+  for (uint32_t e = lane; e < part.splits; e += kWave) mm = fmaxf(mm, ms[e].x);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d, kWave));
+  const float base = mm == -INFINITY ? 0.f : mm;
+  const uint32_t c = (lane % lanes) * 4;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  float z = 0.f;
+  for (uint32_t e = lane / lanes; e < part.splits; e += kWave / lanes) {
+    const float2 x = ms[e];
+    const float f = exp2_raw(x.x - base);
+    if (x.y == 0.f) continue;
+    z += f * x.y;
+    if (c < part.head_dim) {
+      const f32x4 y = *(const f32x4*)(part.row(unit, e) + c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += f * y[r];
+    }
+  }
+  for (uint32_t d = lanes; d < kWave; d <<= 1) {
+    z += __shfl_xor(z, d, kWave);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] += __shfl_xor(o[r], d, kWave);
+  }
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  if (lane < lanes && c < part.head_dim) {
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    t4 v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = (T)(o[r] * inv);
+    *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
+  }
+  if (lse && lane == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
+}
+
+template <typename T, int DP, bool kSelected>
+hipError_t run_decode(const AttendPlan& p, const Cache& c, const Batch& b, const Rows& q,
+                      const Rows& out, const int32_t* sel, uint32_t n_select, float scale,
+                      uint32_t window, bool causal, float* lse, Partial part, hipStream_t s) {
+  hipLaunchKernelGGL((k_kv_decode<T, DP, kSelected>), dim3((uint32_t)p.blocks), dim3(256), 0, s, c,
+                     b, q, out, sel, n_select, scale * kLog2e, window, causal, p.row_tiles, part, lse);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_decode(const AttendPlan& p, const Cache& c, uint32_t dtype, const Batch& b,
+                         const Rows& q, const Rows& out, const int32_t* sel, uint32_t n_select,
+                         float scale, uint32_t window, bool causal, float* lse, Partial part,
+                         hipStream_t s) {
+#define IBP_KV_DECODE(T, DP, SEL) \
+  run_decode<T, DP, SEL>(p, c, b, q, out, sel, n_select, scale, window, causal, lse, part, s)
+#define IBP_KV_DECODE_T(T, SEL)                                          \
+  (c.head_dim <= 64 ? IBP_KV_DECODE(T, 64, SEL)                          \
+                    : c.head_dim <= 128 ? IBP_KV_DECODE(T, 128, SEL) : IBP_KV_DECODE(T, 256, SEL))
+  if (dtype == IBP_KV_F16)
+    return sel ? IBP_KV_DECODE_T(_Float16, true) : IBP_KV_DECODE_T(_Float16, false);
+  return sel ? IBP_KV_DECODE_T(__bf16, true) : IBP_KV_DECODE_T(__bf16, false);
+#undef IBP_KV_DECODE_T
+#undef IBP_KV_DECODE
+}
+
+hipError_t launch_join(uint32_t dtype, const Batch& b, const Rows& out, Partial part, float* lse,
+                       hipStream_t s) {
+  const uint64_t units = (uint64_t)b.n_rows * out.n_heads;
+  const uint32_t lanes = part.head_dim <= 64 ? 16 : part.head_dim <= 128 ? 32 : 64;
+  const dim3 grid((uint32_t)((units + 3) / 4));
+  if (dtype == IBP_KV_F16)
+    hipLaunchKernelGGL(k_kv_join<_Float16>, grid, dim3(256), 0, s, b, out, part, lanes, lse);
+  else
+    hipLaunchKernelGGL(k_kv_join<__bf16>, grid, dim3(256), 0, s, b, out, part, lanes, lse);
+  return hipGetLastError();
+}
+
+}  // namespace kv
+}  // namespace ibp

@@ -1,0 +1,117 @@
+// kv_mfma.h -- matrix-core pieces shared by the attention kernels.
+//
+// Operand layouts (gfx950, wave64).  16x16x32: lane l holds of A row l%16, of B
+// column l%16, k = 8*(l/16) .. +7; of the result column l%16, rows 4*(l/16) + r
+// in register r.  32x32x16: A row / B column l%32, k = 8*(l/32) .. +7; of the
+// result column l%32, row 8*(r/4) + 4*(l/32) + r%4 in register r.
+//
+// Both attention kernels compute S^T = K Q^T and O^T = V^T P^T.  A lane then
+// holds scores of one query only (its column), so the softmax needs no
+// broadcast, and the scores it holds are, once exponentiated, its part of the
+// second product's B operand as they stand: the order of the keys inside a
+// product's k does not matter as long as both operands use the same, so k is
+// numbered the way the first product leaves its rows.
+#pragma once
+
+#include "kv.h"
+
+namespace ibp {
+namespace kv {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <typename T>
+using V8 = typename Vec8<T>::type;
+
+__device__ __forceinline__ f32x4 mfma16(V8<_Float16> a, V8<_Float16> b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma16(V8<__bf16> a, V8<__bf16> b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(V8<_Float16> a, V8<_Float16> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(V8<__bf16> a, V8<__bf16> b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// Transposed LDS read: the 16 lanes of a group point at four rows of 16 values
+// (lane i of the group at row i/4, columns 4*(i%4) .. +3); lane i gets column i of the
+// four rows.
+template <typename T>
+__device__ __forceinline__ s16x4 read_tr(const T* p) {
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+}
+template <typename T>
+__device__ __forceinline__ V8<T> join(s16x4 lo, s16x4 hi) {
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(V8<T>, v);
+}
+
+// max / sum over lanes l, l^32 (and l^16): both halves end with the result.
+__device__ __forceinline__ float max_half(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_quarter(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_half(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_quarter(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 16 B from global memory through a global-address-space pointer.
+template <typename T>
+__device__ __forceinline__ V8<T> load_row8(const T* p) {
+  typedef __attribute__((address_space(1))) const V8<T> global_v8;
+  return *(global_v8*)(uintptr_t)p;
+}
+
+// What a masked or missing key reads: zeros, so that nothing that lies in unused memory
+// (a NaN times a weight of zero is a NaN) reaches the product with the values.
+static __device__ const uint4 zero_row[IBP_KV_MAX_HEAD_DIM / 8] = {};
+
+// Where a row's partial results of the splits of its keys lie in the
+// workspace: float[unit][split][head_dim], then float2[unit][split] of (max,
+// sum); unit = row * heads + head.  Scores in the exponent of 2.
+struct Partial {
+  float* o;
+  float2* ms;
+  uint32_t splits, head_dim;
+  __device__ float* row(uint64_t unit, uint32_t split) const {
+    return o + (unit * splits + split) * head_dim;
+  }
+};
+
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+
+// How a call is run: kernel, tiles of rows, splits of the keys.
+struct AttendPlan {
+  bool few;            // few rows share their keys: kv_decode.hip, else kv_chunk.hip
+  uint32_t row_tiles;  // of a sequence and key head (of a row and key head in lists)
+  uint32_t splits;
+  uint64_t blocks;
+};
+
+hipError_t launch_decode(const AttendPlan& p, const Cache& c, uint32_t dtype, const Batch& b,
+                         const Rows& q, const Rows& out, const int32_t* sel, uint32_t n_select,
+                         float scale, uint32_t window, bool causal, float* lse, Partial part,
+                         hipStream_t s);
+hipError_t launch_join(uint32_t dtype, const Batch& b, const Rows& out, Partial part, float* lse,
+                       hipStream_t s);
+
+}  // namespace kv
+}  // namespace ibp
