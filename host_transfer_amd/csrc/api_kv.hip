@@ -121,9 +121,11 @@ int check_rows(const char* name, const char* what, const ibp_kv_rows* r, uint64_
 int check_batch(const char* name, const ibp_kv_batch* b, const ibp::kv::Cache& c, bool pointers,
                 ibp::kv::Batch* out) {
   if (!b) return set_error(IBP_ERR_NULL, "%s: batch is required", name);
-  if (b->n_rows > 0x7FFFFFFFull || b->n_seqs > 0x7FFFFFFFu || b->max_q > 0x7FFFFFFFu ||
-      b->max_kv > 0x7FFFFFFFu)
-    return set_error(IBP_ERR_SIZE, "%s: n_rows, n_seqs, max_q and max_kv must be below 2^31", name);
+  if (b->n_rows > 0x7FFFFFFFull || b->n_seqs > 0x7FFFFFFFu || b->max_q > 0x7FFFFFFFu)
+    return set_error(IBP_ERR_SIZE, "%s: n_rows, n_seqs and max_q must be below 2^31", name);
+  if (b->max_kv > IBP_KV_MAX_TOKENS)
+    return set_error(IBP_ERR_SIZE, "%s: max_kv %u must be at most %u", name, b->max_kv,
+                     IBP_KV_MAX_TOKENS);
   const uint32_t max_pages = b->max_kv ? c.page.div(b->max_kv - 1) + 1 : 0;
   if (b->n_seqs > 1 && b->table_stride < max_pages)
     return set_error(IBP_ERR_SIZE, "%s: table_stride %llu is below the %u pages of max_kv", name,

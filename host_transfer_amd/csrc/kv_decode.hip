@@ -120,38 +120,48 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
   const T* vbase = (const T*)cache.v + (uint64_t)kh * cache.head_stride;
   T* sv = (T*)s_v[wave];
 
+  // the K and V rows of key t0 + 16 a + col, zeros where no row sees it; bit c of the
+  // result: some row sees key t0 + 16 a + c
+  auto locate = [&](int32_t t0, int a, const T*& kp, const T*& vp) -> uint32_t {
+    int32_t j = t0 + a * 16 + (int32_t)col;
+    bool see = j < end;
+    if (kSelected) {
+      int32_t pg = -1;
+      uint32_t e = 0;
+      if (see) {
+        e = cache.page.div((uint32_t)j);
+        pg = list[e];
+        if (e > 0 && list[e - 1] >= pg) pg = -1;
+      }
+      see = pg >= 0 && (uint32_t)pg < b.max_pages;
+      j = see ? pg * (int32_t)cache.page.d + (j - (int32_t)(e * cache.page.d)) : 0;
+    }
+    see = see && j >= lo_a && j < hi_e;
+    int32_t id = -1;
+    uint32_t page = 0;
+    if (see) {
+      page = cache.page.div((uint32_t)j);
+      id = table[page];
+    }
+    see = id >= 0 && (uint32_t)id < cache.n_pages;
+    const uint64_t at = (uint64_t)(uint32_t)id * cache.page_stride +
+                        (uint64_t)((uint32_t)j - page * cache.page.d) * cache.token_stride;
+    kp = see ? kbase + at : zeros;
+    vp = see ? vbase + at : zeros;
+    return (uint32_t)__ballot(see) & 0xFFFFu;
+  };
+  // this lane's part of a transposed read of V
+  const T* tr_at = sv + (4 * quarter + col / 4) * LD + 4 * (col % 4);
+  bool odd = false;  // values that only some rows see and that are no numbers were left out
+
   for (int32_t t0 = begin + (int32_t)wave * kTile; t0 < end; t0 += kBlockKeys) {
-    // this lane's two keys: t0 + col and t0 + 16 + col
     V8<T> kf[2][KS], vf[2][KS];
-    uint32_t there[2];  // bit c: key c of the 16 can be seen by a row of the tile
+    uint32_t there[2];
     bool plain = true;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      int32_t j = t0 + a * 16 + (int32_t)col;
-      bool see = j < end;
-      if (kSelected) {
-        int32_t pg = -1;
-        uint32_t e = 0;
-        if (see) {
-          e = cache.page.div((uint32_t)j);
-          pg = list[e];
-          if (e > 0 && list[e - 1] >= pg) pg = -1;
-        }
-        see = pg >= 0 && (uint32_t)pg < b.max_pages;
-        j = see ? pg * (int32_t)cache.page.d + (j - (int32_t)(e * cache.page.d)) : 0;
-      }
-      see = see && j >= lo_a && j < hi_e;
-      int32_t id = -1;
-      uint32_t page = 0;
-      if (see) {
-        page = cache.page.div((uint32_t)j);
-        id = table[page];
-      }
-      see = id >= 0 && (uint32_t)id < cache.n_pages;
-      const uint64_t at = (uint64_t)(uint32_t)id * cache.page_stride +
-                          (uint64_t)((uint32_t)j - page * cache.page.d) * cache.token_stride;
-      const T* kp = see ? kbase + at : zeros;
-      const T* vp = see ? vbase + at : zeros;
+      const T *kp, *vp;
+      there[a] = locate(t0, a, kp, vp);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const uint32_t c = (k * 4 + quarter) * 8;
@@ -162,7 +172,6 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
         const uint32_t c = (k * 4 + quarter) * 8;
         vf[a][k] = load_row8(c < hd ? vp + c : zeros);
       }
-      there[a] = (uint32_t)__ballot(see) & 0xFFFFu;
       plain = plain && there[a] == 0xFFFFu;
     }
     // every row sees every key of the tile?  (in lists, one row: `see` said all of it)
@@ -174,6 +183,19 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
       sc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) sc[a] = mfma16(kf[a][k], qf[k], sc[a]);
+    }
+    settle(sc[0], sc[1]);
+    if (!kSelected && !plain) {  // (a list has one row: what it does not see is zeros)
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int32_t j = t0 + a * 16 + (int32_t)col;
+        if (j < lo_e || j >= hi_a)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            odd = odd || any_odd<T>(vf[a][k]);
+            vf[a][k] = finite_part<T>(vf[a][k]);
+          }
+      }
     }
     // V to LDS, row = key of the tile
 #pragma unroll
@@ -224,55 +246,46 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
       p[e] = (T)y;  // <= 1: half a step of the dtype, relative, as the output's own rounding
     }
     wave_sync();
-    if (!kSelected && !plain) {
-      // A key that some rows see and others do not may hold an infinity or a
-      // NaN: times the others' weight of zero it would reach them too.  Such
-      // values are added to the rows that see them here, and are zeros in LDS.
-      bool odd[2];
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+      o[t] = mfma16(join<T>(read_tr(tr_at + t * 16), read_tr(tr_at + t * 16 + 16 * LD)), p, o[t]);
+    wave_sync();
+  }
+
+  settle(o);
+  if (!kSelected && __any(odd)) {
+    for (int32_t t0 = begin + (int32_t)wave * kTile; t0 < end; t0 += kBlockKeys) {
+      if (t0 >= lo_e && t0 + kTile <= hi_a) continue;
+      V8<T> sees;
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const int32_t j = t0 + a * 16 + (int32_t)col;
-        odd[a] = false;
-        if (j < lo_e || j >= hi_a)
+        const T *kp, *vp;
+        const uint32_t there = locate(t0, a, kp, vp);
+        const int32_t mine = t0 + a * 16 + (int32_t)col;
+        const bool some = mine < lo_e || mine >= hi_a;
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) odd[a] |= !isfinite((float)vf[a][k][e]);
-      }
-      const uint64_t any[2] = {__ballot(odd[0]), __ballot(odd[1])};
-      if (any[0] | any[1]) {
-        for (uint32_t kk = 0; kk < kTile; ++kk) {
-          const uint64_t who = any[kk / 16];
-          if (!(((who | (who >> 16) | (who >> 32) | (who >> 48)) >> (kk % 16)) & 1u)) continue;
-          const int32_t j = t0 + (int32_t)kk;
-          const bool see = j >= lo && j < hi;
-#pragma unroll
-          for (int t = 0; t < DT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float v = to_f32(sv[kk * LD + t * 16 + quarter * 4 + r]);
-              if (see && !isfinite(v)) o[t][r] += v;
-            }
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t c = (k * 4 + quarter) * 8;
+          *(V8<T>*)(sv + (a * 16 + col) * LD + c) =
+              odd_code<T>(load_row8(some && c < hd ? vp + c : zeros));
         }
-        wave_sync();
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
-          if (odd[a])
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (!isfinite((float)vf[a][k][e]))
-                  sv[(a * 16 + col) * LD + (k * 4 + quarter) * 8 + e] = (T)0.f;
-        wave_sync();
+        for (int r = 0; r < 4; ++r) {
+          const int32_t j = t0 + a * 16 + (int32_t)(4 * quarter) + r;
+          sees[a * 4 + r] = (T)(((there >> (4 * quarter + r)) & 1u) && j >= lo && j < hi ? 1.f : 0.f);
+        }
       }
-    }
+      wave_sync();
 #pragma unroll
-    for (int t = 0; t < DT; ++t) {
-      const T* at = sv + (4 * quarter + col / 4) * LD + t * 16 + 4 * (col % 4);
-      o[t] = mfma16(join<T>(read_tr(at), read_tr(at + 16 * LD)), p, o[t]);
+      for (int t = 0; t < DT; ++t) {
+        f32x4 n = f32x4{0.f, 0.f, 0.f, 0.f};
+        n = mfma16(join<T>(read_tr(tr_at + t * 16), read_tr(tr_at + t * 16 + 16 * LD)), sees, n);
+        settle(n);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[t][r] = add_odd(o[t][r], n[r]);
+      }
+      wave_sync();
     }
-    wave_sync();
   }
 
   // the four waves' results together: rows of DP floats in the V tiles

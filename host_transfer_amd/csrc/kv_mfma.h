@@ -38,6 +38,30 @@ __device__ __forceinline__ f32x16 mfma32(V8<__bf16> a, V8<__bf16> b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// Waits until results of matrix instructions can be read by others.  The
+// compiler does so itself where the reader follows in the same basic block; where a
+// branch lay between (the scores' masks) its output had no wait on the
+// taken path, and the scores read were old ones now and then.  20 wait states
+// cover the longest form used here (19 for 16 passes).
+__device__ __forceinline__ void settle(f32x4& a, f32x4& b) {
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" : "+v"(a), "+v"(b));
+}
+__device__ __forceinline__ void settle(f32x4& a) {
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" : "+v"(a));
+}
+__device__ __forceinline__ void settle(f32x16& a) {
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" : "+v"(a));
+}
+__device__ __forceinline__ void settle(f32x16& a, f32x16& b) {
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" : "+v"(a), "+v"(b));
+}
+template <typename V, int N>
+__device__ __forceinline__ void settle(V (&a)[N]) {
+#pragma unroll
+  for (int i = 0; i + 1 < N; i += 2) settle(a[i], a[i + 1]);
+  if (N % 2) settle(a[N - 1]);
+}
+
 // Transposed LDS read: the 16 lanes of a group point at four rows of 16 values
 // (lane i of the group at row i/4, columns 4*(i%4) .. +3); lane i gets column i of the
 // four rows.
@@ -84,6 +108,42 @@ __device__ __forceinline__ V8<T> load_row8(const T* p) {
 // (a NaN times a weight of zero is a NaN) reaches the product with the values.
 static __device__ const uint4 zero_row[IBP_KV_MAX_HEAD_DIM / 8] = {};
 
+// Infinities and NaNs among values that only some of a product's rows see.  Such a
+// value times the weight of zero of a row that does not see it is a NaN, so it stays
+// out of the product (finite_part), and a second product of its code with the
+// rows' visibility (1 or 0) counts, exactly for up to 127 keys, what each output sees:
+// +inf counts 1, -inf 128, NaN 16384 (add_odd).
+template <typename T>
+__device__ __forceinline__ V8<T> finite_part(V8<T> v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (!isfinite((float)v[e])) v[e] = (T)0.f;
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ V8<T> odd_code(V8<T> v) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = (float)v[e];
+    v[e] = (T)(isfinite(x) ? 0.f : x > 0.f ? 1.f : x < 0.f ? 128.f : 16384.f);
+  }
+  return v;
+}
+__device__ __forceinline__ float add_odd(float o, float count) {
+  const uint32_t n = (uint32_t)count;
+  if (n & 127u) o += INFINITY;
+  if ((n >> 7) & 127u) o -= INFINITY;
+  if (n >> 14) o = NAN;
+  return o;
+}
+template <typename T>
+__device__ __forceinline__ bool any_odd(V8<T> v) {
+  bool odd = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) odd = odd || !isfinite((float)v[e]);
+  return odd;
+}
+
 // Where a row's partial results of the splits of its keys lie in the
 // workspace: float[unit][split][head_dim], then float2[unit][split] of (max,
 // sum); unit = row * heads + head.  Scores in the exponent of 2.
@@ -110,6 +170,10 @@ hipError_t launch_decode(const AttendPlan& p, const Cache& c, uint32_t dtype, co
                          const Rows& q, const Rows& out, const int32_t* sel, uint32_t n_select,
                          float scale, uint32_t window, bool causal, float* lse, Partial part,
                          hipStream_t s);
+constexpr uint32_t kChunkRows = 128;  // rows of a workgroup of kv_chunk.hip
+hipError_t launch_chunk(const AttendPlan& p, const Cache& c, uint32_t dtype, const Batch& b,
+                        const Rows& q, const Rows& out, float scale, uint32_t window, bool causal,
+                        float* lse, Partial part, hipStream_t s);
 hipError_t launch_join(uint32_t dtype, const Batch& b, const Rows& out, Partial part, float* lse,
                        hipStream_t s);
 

@@ -43,6 +43,7 @@ extern "C" {
 #define IBP_KV_MAX_HEAD_DIM 256u
 #define IBP_KV_MAX_PAGE_TOKENS 65536u
 #define IBP_KV_MAX_SELECT 4096u
+#define IBP_KV_MAX_TOKENS (1u << 30)  /* of one sequence */
 
 /* A paged cache: key token `slot` of page p, head h, starts at
  * k + p*page_stride + slot*token_stride + h*head_stride, values likewise.
@@ -80,7 +81,7 @@ typedef struct {
  *   max_q       at least every q_start[s+1] - q_start[s]; new tokens of a
  *               sequence past the first max_q are left as they were.
  *   max_kv      at least every kv_len[s]; tokens at positions >= max_kv are
- *               not read.  < 2^31. */
+ *               not read.  At most IBP_KV_MAX_TOKENS. */
 typedef struct {
     const int32_t *q_start, *kv_len, *page_table;
     uint64_t table_stride, n_rows;
