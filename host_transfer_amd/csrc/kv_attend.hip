@@ -22,6 +22,7 @@ hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_
   const uint64_t want = (uint64_t)di.cus * (p->few ? 4 : 2);
   uint64_t splits = base ? (want + base - 1) / base : 1;
   if (splits > keys / (p->few ? 256 : 512)) splits = keys / (p->few ? 256 : 512);
+  if (splits > kMaxSplits) splits = kMaxSplits;
   p->splits = splits < 1 ? 1 : (uint32_t)splits;
   p->blocks = base * p->splits;
   return p->blocks > 0x7FFFFFFFull ? hipErrorInvalidConfiguration : hipSuccess;

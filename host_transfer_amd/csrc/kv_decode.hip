@@ -342,51 +342,78 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
   }
 }
 
-// The splits of a row together: a wave per (row, head), 16, 32 or 64 lanes (four
-// channels each) a split, the splits in turn.
+// The splits of a row together: a workgroup per (row, head).  Each split's factor first, from
+// the maxima; then 16, 32 or 64 lanes (four channels each) a split, as many splits at
+// a time as the workgroup holds.
 template <typename T>
 __global__ __launch_bounds__(256) void k_kv_join(Batch b, Rows out, Partial part, uint32_t lanes,
                                                  float* __restrict__ lse) {
-  const uint32_t lane = threadIdx.x % kWave;
-  const uint64_t unit = (uint64_t)blockIdx.x * 4 + threadIdx.x / kWave;
-  if (unit >= (uint64_t)b.n_rows * out.n_heads) return;
+  __shared__ float s_f[kMaxSplits];
+  __shared__ float s_red[kWaves];
+  __shared__ f32x4 s_o[256];
+  const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const uint64_t unit = blockIdx.x;
   const uint32_t row = (uint32_t)(unit / out.n_heads), head = (uint32_t)(unit % out.n_heads);
-  const int32_t s = seq_of_row(b, (int32_t)row);
-  if (s < 0) return;
+  if (seq_of_row(b, (int32_t)row) < 0) return;
   const float2* ms = part.ms + unit * part.splits;
+  float2 x[kMaxSplits / 256];
   float mm = -INFINITY;
-  for (uint32_t e = lane; e < part.splits; e += kWave) mm = fmaxf(mm, ms[e].x);
+#pragma unroll
+  for (uint32_t a = 0; a < kMaxSplits / 256; ++a) {
+    const uint32_t e = tid + a * 256;
+    x[a] = e < part.splits ? ms[e] : make_float2(-INFINITY, 0.f);
+    mm = fmaxf(mm, x[a].x);
+  }
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d, kWave));
+  if (lane == 0) s_red[wave] = mm;
+  __syncthreads();
+  mm = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  __syncthreads();
   const float base = mm == -INFINITY ? 0.f : mm;
-  const uint32_t c = (lane % lanes) * 4;
-  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
   float z = 0.f;
-  for (uint32_t e = lane / lanes; e < part.splits; e += kWave / lanes) {
-    const float2 x = ms[e];
-    const float f = exp2_raw(x.x - base);
-    if (x.y == 0.f) continue;
-    z += f * x.y;
-    if (c < part.head_dim) {
-      const f32x4 y = *(const f32x4*)(part.row(unit, e) + c);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] += f * y[r];
+  for (uint32_t a = 0; a < kMaxSplits / 256; ++a) {
+    const uint32_t e = tid + a * 256;
+    const float f = exp2_raw(x[a].x - base);
+    if (e < part.splits) {
+      s_f[e] = f;
+      z += f * x[a].y;
     }
   }
-  for (uint32_t d = lanes; d < kWave; d <<= 1) {
-    z += __shfl_xor(z, d, kWave);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] += __shfl_xor(o[r], d, kWave);
+  for (int d = 1; d < kWave; d <<= 1) z += __shfl_xor(z, d, kWave);
+  if (lane == 0) s_red[wave] = z;
+  __syncthreads();
+  z = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+  const uint32_t c = (tid % lanes) * 4;
+  const uint32_t at_once = 256 / lanes;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (c < part.head_dim) {
+#pragma unroll 4
+    for (uint32_t e = tid / lanes; e < part.splits; e += at_once) {
+      const float f = s_f[e];
+      const f32x4 y = *(const f32x4*)(part.row(unit, e) + c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += f == 0.f ? 0.f : f * y[r];
+    }
   }
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-  if (lane < lanes && c < part.head_dim) {
+  s_o[tid] = o;
+  __syncthreads();
+  if (tid < lanes && c < part.head_dim) {
+    for (uint32_t a = 1; a < at_once; ++a) {
+      const f32x4 y = s_o[a * lanes + tid];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += y[r];
+    }
+    const float inv = z == 0.f ? 0.f : 1.f / z;
     typedef T t4 __attribute__((ext_vector_type(4)));
     t4 v;
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] = (T)(o[r] * inv);
     *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
   }
-  if (lse && lane == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
+  if (lse && tid == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
 }
 
 template <typename T, int DP, bool kSelected>
@@ -420,7 +447,7 @@ hipError_t launch_join(uint32_t dtype, const Batch& b, const Rows& out, Partial 
                        hipStream_t s) {
   const uint64_t units = (uint64_t)b.n_rows * out.n_heads;
   const uint32_t lanes = part.head_dim <= 64 ? 16 : part.head_dim <= 128 ? 32 : 64;
-  const dim3 grid((uint32_t)((units + 3) / 4));
+  const dim3 grid((uint32_t)units);
   if (dtype == IBP_KV_F16)
     hipLaunchKernelGGL(k_kv_join<_Float16>, grid, dim3(256), 0, s, b, out, part, lanes, lse);
   else

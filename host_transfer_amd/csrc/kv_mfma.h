@@ -158,6 +158,8 @@ struct Partial {
 
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
+constexpr uint32_t kMaxSplits = 1024;
+
 // How a call is run: kernel, tiles of rows, splits of the keys.
 struct AttendPlan {
   bool few;            // few rows share their keys: kv_decode.hip, else kv_chunk.hip
