@@ -173,15 +173,18 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(Cache 
     if (active && t0 < w_hi && t0 + kKeys > w_lo) {
       f32x16 sc[2];
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
+      for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int r = 0; r < 16; ++r) sc[a][r] = 0.f;
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
           const V8<T> kf = *(const V8<T>*)(sk + (a * 32 + col) * LK + k * 16 + half * 8);
           sc[a] = mfma32(kf, qf[k], sc[a]);
         }
-      }
+      __builtin_amdgcn_s_setprio(0);
       settle(sc[0], sc[1]);
       // register r of tile a: key t0 + 32 a + 8 (r / 4) + 4 half + r % 4
       if (!(seen == ~0ull && t0 >= full_lo && t0 + kKeys <= full_hi)) {
@@ -225,13 +228,15 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(Cache 
           p[a * 2 + r / 8][r % 8] = (T)y;
         }
       const uint16_t* at = sv + tr_at;
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int t = 0; t < DT; ++t)
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int t = 0; t < DT; ++t) {
           const T* v = (const T*)at + 16 * k * LV + t * 32;
           o[t] = mfma32(join<T>(read_tr(v), read_tr(v + 8 * LV)), p[k], o[t]);
         }
+      __builtin_amdgcn_s_setprio(0);
     }
   }
 

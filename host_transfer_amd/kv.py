@@ -70,19 +70,34 @@ for _name, _args in _SIGS.items():
 EXPORTED = tuple(_SIGS)
 
 
-def _on_device(name, t, dtype):
-    """t as a device tensor of this dtype on the current device."""
+# the current stream's handle without building a torch Stream around it (some microseconds)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device():
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _stream(s, dev):
+    if s is None and _raw_stream is not None and dev >= 0:
+        return _raw_stream(dev)
+    return ibp._stream(s)
+
+
+def _on_device(name, t, dtype, dev):
+    """Checks that t is of this dtype and on the current device `dev`."""
     if t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} needed, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: a GPU tensor is needed")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: on device {t.get_device()}, not on the current one")
-    return t
+    d = t.get_device()
+    if d != dev:
+        raise ValueError(f"{name}: a GPU tensor is needed" if d < 0 else
+                         f"{name}: on device {d}, not on the current one")
 
 
 def _strides(t):
     """Strides, those of axes of size 1 as if packed (they address nothing)."""
+    if 1 not in t.shape:
+        return t.stride()
     out, inner = [], 1
     for n, s in zip(reversed(t.shape), reversed(t.stride())):
         out.append(s if n > 1 else inner)
@@ -90,12 +105,12 @@ def _strides(t):
     return tuple(reversed(out))
 
 
-def _plain(name, t, dtype, numel):
+def _plain(name, t, dtype, numel, dev):
     """Pointer of a contiguous device array with at least numel elements; other
     pointers as they are."""
-    if t is None or not isinstance(t, torch.Tensor):
+    if not isinstance(t, torch.Tensor):
         return ibp._ptr(t)
-    _on_device(name, t, dtype)
+    _on_device(name, t, dtype, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous tensor is needed")
     if t.numel() < numel:
@@ -112,8 +127,9 @@ class Cache:
             raise ValueError("k and v must both be (n_pages, page_tokens, n_heads, head_dim)")
         if k.dtype not in _DTYPES:
             raise ValueError(f"k: float16 or bfloat16 needed, got {k.dtype}")
-        _on_device("k", k, k.dtype)
-        _on_device("v", v, k.dtype)
+        dev = _device()
+        _on_device("k", k, k.dtype, dev)
+        _on_device("v", v, k.dtype, dev)
         s = _strides(k)
         if s != _strides(v):
             raise ValueError("k and v must have the same strides")
@@ -161,7 +177,7 @@ class Batch:
     def __init__(self, q_start, kv_len, page_table, max_q, max_kv):
         n = kv_len.numel()
         for name, t in (("q_start", q_start), ("kv_len", kv_len), ("page_table", page_table)):
-            _on_device(name, t, torch.int32)
+            _on_device(name, t, torch.int32, _device())
         if q_start.dim() != 1 or kv_len.dim() != 1 or q_start.numel() != n + 1 or \
                 not q_start.is_contiguous() or not kv_len.is_contiguous():
             raise ValueError("q_start must be (n_seqs + 1,), kv_len (n_seqs,), both contiguous")
@@ -195,65 +211,79 @@ class Batch:
         return _CBatch(*self._args, n_rows, self.n_seqs, self.max_q, self.max_kv)
 
 
-def _rows(name, cache, t, n_tokens=None):
+def _rows(name, cache, t, n_tokens, dev):
     """(struct, tokens) of a (tokens, heads, head_dim) tensor or a Rows."""
     if isinstance(t, Rows):
+        if n_tokens is None:
+            raise ValueError(f"{name}: the number of tokens is needed with Rows")
         return t._c, n_tokens
-    if t.dim() != 3 or t.shape[2] != cache.head_dim:
-        raise ValueError(f"{name}: (tokens, heads, {cache.head_dim}) needed, got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"{name}: (tokens, heads, {cache.head_dim}) needed, got {tuple(shape)}")
     if cache.torch_dtype is not None:
-        _on_device(name, t, cache.torch_dtype)
-    if n_tokens is not None and t.shape[0] != n_tokens:
-        raise ValueError(f"{name}: {n_tokens} tokens needed, got {t.shape[0]}")
+        _on_device(name, t, cache.torch_dtype, dev)
+    n = shape[0]
+    if n_tokens is not None and n != n_tokens:
+        raise ValueError(f"{name}: {n_tokens} tokens needed, got {n}")
     s = _strides(t)
     if s[2] != 1:
         raise ValueError(f"{name}: channels must be contiguous")
-    return _CRows(t.data_ptr(), s[0], s[1], t.shape[1]), t.shape[0]
+    return _CRows(t.data_ptr(), s[0], s[1], shape[1]), n
 
 
-def _of_dtype(name, cache, t, numel):
-    if isinstance(t, torch.Tensor) and cache.torch_dtype is not None:
-        return _plain(name, t, cache.torch_dtype, numel)
-    return ibp._ptr(t)
+def _of_dtype(name, cache, t, numel, dev):
+    if cache.torch_dtype is None:
+        return ibp._ptr(t)
+    return _plain(name, t, cache.torch_dtype, numel, dev)
 
 
-def _workspace(ws):
+def _workspace(ws, dev):
     if ws is None:
         return None, 0
-    _on_device("workspace", ws, ws.dtype)
+    _on_device("workspace", ws, ws.dtype, dev)
     if not ws.is_contiguous():
         raise ValueError("workspace: a contiguous tensor is needed")
     return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _sel(sel, cache, n, n_select, dev):
+    if isinstance(sel, torch.Tensor):
+        if sel.dim() != 3 or tuple(sel.shape[:2]) != (n, cache.n_heads):
+            raise ValueError(f"sel: ({n}, {cache.n_heads}, n_select) needed, got {tuple(sel.shape)}")
+        n_select = sel.shape[2]
+    elif n_select is None:
+        raise ValueError("n_select is needed with a pointer")
+    return _plain("sel", sel, torch.int32, 0, dev), n_select
 
 
 def append(cache, k, v, slots, q=None, q_out=None, positions=None, rope=None, flags=0, q_norm=None,
            k_norm=None, eps=1e-6, n_tokens=None, n_positions=None, rope_dim=None, stream=None):
     """k, v, q, q_out: (tokens, heads, head_dim) tensors or Rows (n_tokens is then needed); rope:
     float32 (n_positions, rope_dim), cosines then sines; slots, positions: int64 (tokens,)."""
-    kr, n = _rows("k", cache, k, n_tokens)
-    if n is None:
-        raise ValueError("n_tokens is needed with Rows")
-    vr, _ = _rows("v", cache, v, n)
-    qr, _ = (None, n) if q is None else _rows("q", cache, q, n)
-    qo, _ = (None, n) if q_out is None else _rows("q_out", cache, q_out, n)
+    dev = _device()
+    kr, n = _rows("k", cache, k, n_tokens, dev)
+    vr, _ = _rows("v", cache, v, n, dev)
+    qr = None if q is None else _rows("q", cache, q, n, dev)[0]
+    qo = None if q_out is None else _rows("q_out", cache, q_out, n, dev)[0]
     if isinstance(rope, torch.Tensor):
         if rope.dim() != 2:
             raise ValueError("rope must be (n_positions, rope_dim)")
         n_positions, rope_dim = rope.shape
     ibp._check(ibp._lib.ibp_kv_append(
-        cache._c, kr, vr, qr, qo, _plain("slots", slots, torch.int64, n),
-        _plain("positions", positions, torch.int64, n), n,
-        _plain("rope", rope, torch.float32, 0), n_positions or 0, rope_dim or 0,
-        _of_dtype("q_norm", cache, q_norm, cache.head_dim),
-        _of_dtype("k_norm", cache, k_norm, cache.head_dim), eps, flags, ibp._stream(stream)))
+        cache._c, kr, vr, qr, qo, _plain("slots", slots, torch.int64, n, dev),
+        _plain("positions", positions, torch.int64, n, dev), n,
+        _plain("rope", rope, torch.float32, 0, dev), n_positions or 0, rope_dim or 0,
+        _of_dtype("q_norm", cache, q_norm, cache.head_dim, dev),
+        _of_dtype("k_norm", cache, k_norm, cache.head_dim, dev), eps, flags, _stream(stream, dev)))
 
 
 def page_bounds(cache, batch, bounds, stream=None):
     """bounds: (n_pages, n_heads, 2, head_dim) of the cache's dtype."""
+    dev = _device()
     ibp._check(ibp._lib.ibp_kv_page_bounds(
         cache._c, batch._c(cache, 0),
-        _of_dtype("bounds", cache, bounds, cache.n_pages * cache.n_heads * 2 * cache.head_dim),
-        ibp._stream(stream)))
+        _of_dtype("bounds", cache, bounds, cache.n_pages * cache.n_heads * 2 * cache.head_dim, dev),
+        _stream(stream, dev)))
 
 
 def attend_workspace(cache, batch, n_rows, n_q_heads) -> int:
@@ -267,14 +297,13 @@ def attend(cache, batch, q, out, scale, window=0, flags=CAUSAL, lse=None, worksp
            n_rows=None, stream=None):
     """q, out: (rows, heads, head_dim) tensors or Rows (n_rows is then needed); lse: float32
     (rows, heads); workspace: a device tensor of at least attend_workspace() bytes."""
-    qr, n = _rows("q", cache, q, n_rows)
-    if n is None:
-        raise ValueError("n_rows is needed with Rows")
-    orow, _ = _rows("out", cache, out, n)
-    ws, ws_bytes = _workspace(workspace)
+    dev = _device()
+    qr, n = _rows("q", cache, q, n_rows, dev)
+    orow, _ = _rows("out", cache, out, n, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     ibp._check(ibp._lib.ibp_kv_attend(
         cache._c, batch._c(cache, n), qr, orow, scale, window, flags,
-        _plain("lse", lse, torch.float32, n * qr.n_heads), ws, ws_bytes, ibp._stream(stream)))
+        _plain("lse", lse, torch.float32, n * qr.n_heads, dev), ws, ws_bytes, _stream(stream, dev)))
 
 
 def select_workspace(cache, batch, n_rows, n_select) -> int:
@@ -288,22 +317,18 @@ def select(cache, batch, bounds, q, sel, n_first=1, n_last=1, n_select=None, n_b
            workspace=None, n_rows=None, stream=None):
     """bounds: (n_bounds, n_heads, 2, head_dim) of the cache's dtype; sel: int32 (rows, n_heads,
     n_select)."""
-    qr, n = _rows("q", cache, q, n_rows)
-    if n is None:
-        raise ValueError("n_rows is needed with Rows")
-    if isinstance(sel, torch.Tensor):
-        if sel.dim() != 3 or tuple(sel.shape[:2]) != (n, cache.n_heads):
-            raise ValueError(f"sel: ({n}, {cache.n_heads}, n_select) needed, got {tuple(sel.shape)}")
-        n_select = sel.shape[2]
+    dev = _device()
+    qr, n = _rows("q", cache, q, n_rows, dev)
+    sel_p, n_select = _sel(sel, cache, n, n_select, dev)
     if isinstance(bounds, torch.Tensor):
         if bounds.dim() != 4 or tuple(bounds.shape[1:]) != (cache.n_heads, 2, cache.head_dim):
             raise ValueError(f"bounds: (pages, {cache.n_heads}, 2, {cache.head_dim}) needed, got "
                              f"{tuple(bounds.shape)}")
         n_bounds = bounds.shape[0]
-    ws, ws_bytes = _workspace(workspace)
+    ws, ws_bytes = _workspace(workspace, dev)
     ibp._check(ibp._lib.ibp_kv_select(
-        cache._c, batch._c(cache, n), _of_dtype("bounds", cache, bounds, 0), n_bounds, qr, n_first,
-        n_last, n_select, _plain("sel", sel, torch.int32, 0), ws, ws_bytes, ibp._stream(stream)))
+        cache._c, batch._c(cache, n), _of_dtype("bounds", cache, bounds, 0, dev), n_bounds, qr, n_first,
+        n_last, n_select, sel_p, ws, ws_bytes, _stream(stream, dev)))
 
 
 def attend_selected_workspace(cache, batch, n_rows, n_q_heads, n_select) -> int:
@@ -317,15 +342,11 @@ def attend_selected_workspace(cache, batch, n_rows, n_q_heads, n_select) -> int:
 def attend_selected(cache, batch, q, sel, out, scale, lse=None, n_select=None, workspace=None,
                     n_rows=None, stream=None):
     """As attend (causal), over the pages that sel lists for each row and key head."""
-    qr, n = _rows("q", cache, q, n_rows)
-    if n is None:
-        raise ValueError("n_rows is needed with Rows")
-    orow, _ = _rows("out", cache, out, n)
-    if isinstance(sel, torch.Tensor):
-        if sel.dim() != 3 or tuple(sel.shape[:2]) != (n, cache.n_heads):
-            raise ValueError(f"sel: ({n}, {cache.n_heads}, n_select) needed, got {tuple(sel.shape)}")
-        n_select = sel.shape[2]
-    ws, ws_bytes = _workspace(workspace)
+    dev = _device()
+    qr, n = _rows("q", cache, q, n_rows, dev)
+    orow, _ = _rows("out", cache, out, n, dev)
+    sel_p, n_select = _sel(sel, cache, n, n_select, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
     ibp._check(ibp._lib.ibp_kv_attend_selected(
-        cache._c, batch._c(cache, n), qr, orow, _plain("sel", sel, torch.int32, 0), n_select, scale,
-        _plain("lse", lse, torch.float32, n * qr.n_heads), ws, ws_bytes, ibp._stream(stream)))
+        cache._c, batch._c(cache, n), qr, orow, sel_p, n_select, scale,
+        _plain("lse", lse, torch.float32, n * qr.n_heads, dev), ws, ws_bytes, _stream(stream, dev)))
