@@ -32,191 +32,221 @@ __device__ __forceinline__ Range page_range(const Cache& cache, const Batch& b, 
   return r;
 }
 
-// A lane exchange inside rows of 16 lanes, as two 32-bit moves in the vector ALU.
+// Lane exchanges inside rows of 16 lanes, in the vector ALU: x of lane l ^ D.
 template <int kCtrl, int kBanks>
-__device__ __forceinline__ double dpp64(double old, double x) {
-  const uint64_t u = (uint64_t)__double_as_longlong(x), o = (uint64_t)__double_as_longlong(old);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)u, kCtrl,
-                                                            0xF, kBanks, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)(o >> 32),
-                                                            (int)(uint32_t)(u >> 32), kCtrl, 0xF,
-                                                            kBanks, false);
-  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)x, kCtrl, 0xF, kBanks, false);
 }
-// x of lane l ^ D
 template <int D>
-__device__ __forceinline__ double xor_lane(double x) {
-  if constexpr (D == 1) return dpp64<0xB1, 0xF>(x, x);        // quad_perm 1,0,3,2
-  if constexpr (D == 2) return dpp64<0x4E, 0xF>(x, x);        // quad_perm 2,3,0,1
-  if constexpr (D == 4) {                                     // row_shl / row_shr by 4
-    const double y = dpp64<0x104, 0x5>(x, x);                 // banks 0, 2: from l + 4
-    return dpp64<0x114, 0xA>(y, x);                           // banks 1, 3: from l - 4
-  }
-  if constexpr (D == 8) return dpp64<0x128, 0xF>(x, x);       // row_ror by 8
-  const uint64_t u = (uint64_t)__double_as_longlong(x);       // 16: the other row of a pair
-  const auto a = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
-  const auto b = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
-  const bool up = (__lane_id() & 16) != 0;
-  const uint32_t lo = up ? a[0] : a[1], hi = up ? b[0] : b[1];
-  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+__device__ __forceinline__ uint32_t xor_lane(uint32_t x) {
+  if constexpr (D == 1) return dpp<0xB1, 0xF>(x, x);  // quad_perm 1,0,3,2
+  if constexpr (D == 2) return dpp<0x4E, 0xF>(x, x);  // quad_perm 2,3,0,1
+  if constexpr (D == 4)                               // banks 0, 2: row_shl 4; 1, 3: row_shr 4
+    return dpp<0x114, 0xA>(dpp<0x104, 0x5>(x, x), x);
+  return dpp<0x128, 0xF>(x, x);                       // row_ror 8
+}
+template <int D>
+__device__ __forceinline__ float max_lane(float x) {
+  return fmaxf(x, __uint_as_float(xor_lane<D>(__float_as_uint(x))));
 }
 __device__ __forceinline__ double nan_max64(double a, double b) {
   return (b > a || b != b) ? b : a;
 }
 
-constexpr int kVecs = 4;          // query vectors (row, head) a wave scores at a time
-constexpr int kScorePages = 256;  // pages of a workgroup
-constexpr int kAhead = 3;         // steps that are in flight ahead of the one worked on
+constexpr int kPages = 64;                     // pages of a wave
+constexpr uint32_t kScorePages = 4 * kPages;   // of a workgroup
 
-// Scores of 256 pages (64 a wave) for the vectors of a tile of rows: one row, or as many as
-// make four vectors.  LP lanes hold a page's bounds, eight channels each, so that a
-// wave reads 64 / LP pages at a time, whole lines, three steps ahead; the vectors stay in
-// registers.  With m = hi + lo and r = hi - lo, max(q lo, q hi) is (q m + |q| r) / 2
-// wherever all is finite: two fused multiply-adds a channel and vector, at the same rate in 64
-// bits as in 32, with one register pair for q and its magnitude.  (Where the sum is not finite
-// it is formed again as the definition has it.)  The order of the sum is the same for every
-// page, so equal bounds have equal scores.  The four vectors' sums over LP lanes are
-// folded together: two exchanges leave each quarter of the lanes with one vector, the rest
-// are butterflies, all in the vector ALU.
+// The workspace of a call: per (row, key head) `pages` 32-bit scores, one bound of the
+// terms' sum for every kPages of them, and room for exact scores' images.
+struct Scores {
+  float* s;
+  float* mag;
+  uint64_t* exact;
+  uint32_t pages;  // a multiple of kScorePages
+};
+
+// Scores of 256 pages (64 a wave) in 32 bits, for as many rows of a key head as make 16
+// vectors (a row's group padded to a power of two; a larger group in several passes), and the
+// largest sum of the terms' magnitudes, from which k_kv_pick bounds the scores' error.
 //
-// 64-bit sums decide which pages are read, so that the choice does not depend on the
-// order of a 32-bit sum.
-template <typename T, int LP>
-__global__ __launch_bounds__(256, 2) void k_kv_score(Cache cache, Batch b, const T* __restrict__ bounds,
-                                                     uint32_t n_bounds, Rows q, uint32_t n_first,
-                                                     uint32_t n_last, uint32_t n_select,
-                                                     uint32_t row_tiles, uint32_t rows_per_tile,
-                                                     uint32_t page_blocks,
-                                                     uint64_t* __restrict__ keys) {
-  constexpr int PP = kWave / LP;  // pages at a time
+// With q split into its positive and negative part the score is a product of [hi, lo] rows
+// with [q+, q-] columns for the matrix cores: max(q lo, q hi) = q+ hi + q- lo where all is
+// finite, and a lane reads the bounds as k_kv_decode reads K.  The magnitudes are the same
+// product of absolute values.  So the bounds are read once, at the rate of memory, for
+// 16 vectors; 64-bit sums of all pages in the vector ALU took 40 against 25 us for 8 rows of 32
+// heads over up to 4,096 pages (100 MB of bounds), and 146 against 32 us where 280 rows share
+// two sequences' pages.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void k_kv_score(Cache cache, Batch b, const T* __restrict__ bounds,
+                                                  uint32_t n_bounds, Rows q, uint32_t n_first,
+                                                  uint32_t n_last, uint32_t n_select,
+                                                  uint32_t row_tiles, uint32_t padded_log2,
+                                                  Scores out) {
+  constexpr int KS = DP / 32;
   typedef V8<T> v8;
   const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
-  const uint32_t c = lane % LP, sub = lane / LP;
+  const uint32_t col = lane % 16, quarter = lane / 16;
   const uint32_t group = q.n_heads / cache.n_heads, hd = cache.head_dim;
   uint32_t u = blockIdx.x;
   const uint32_t h = u % cache.n_heads;
   u /= cache.n_heads;
-  const uint32_t pb = u % page_blocks;
-  u /= page_blocks;
+  const uint32_t blocks = out.pages / kScorePages;
+  const uint32_t pb = u % blocks;
+  u /= blocks;
   const uint32_t tile = u % row_tiles, s = u / row_tiles;
   const Seq sq = load_seq(b, s);
+  const uint32_t rows_per_tile = 16u >> padded_log2;
   const int32_t i0 = (int32_t)(tile * rows_per_tile);
   const int32_t n_i = min(sq.q_len - i0, (int32_t)rows_per_tile);
   if (n_i <= 0) return;
   // the pages that any row of the tile scores (later rows score as many or more)
   const Range rg = page_range(cache, b, sq, sq.first + i0 + n_i - 1, n_first, n_last);
   if (rg.last + 1 <= (int32_t)n_select) return;
-  const int32_t p0 = (int32_t)(pb * kScorePages + wave * kWave);  // this wave's 64 pages
-  const int32_t lo_p = max(p0, rg.lo), hi_p = min(p0 + kWave, rg.hi);
-  if (lo_p >= hi_p) return;
-  int32_t id = p0 + (int32_t)lane;  // of page p0 + lane; -1: no bounds
-  id = id >= lo_p && id < hi_p ? b.table[(uint64_t)s * b.table_stride + id] : -1;
-  if ((uint32_t)id >= n_bounds) id = -1;
+  const int32_t p0 = (int32_t)(pb * kScorePages + wave * kPages);
+  if (p0 >= rg.hi || p0 + kPages <= rg.lo) return;
 
-  // which row's score a lane ends up with: the vectors of a row lie in all lanes of a page
-  // (three or four), in its halves (two) or its quarters
-  const uint32_t vi = ((c & (LP / 2)) ? 2u : 0u) + ((c & (LP / 4)) ? 1u : 0u);
-  const uint32_t my_i = group >= 3 ? 0 : group == 2 ? vi / 2 : vi;
-  const bool writes = c % (group >= 3 ? LP : group == 2 ? LP / 2 : LP / 4) == 0 && my_i < (uint32_t)n_i;
-  const uint32_t my_row = (uint32_t)(sq.row0 + i0) + my_i;
-  Range own = page_range(cache, b, sq, sq.first + i0 + (int32_t)my_i, n_first, n_last);
-  if (!writes || own.last + 1 <= (int32_t)n_select) own.hi = own.lo;
-  uint64_t* my_keys = keys + ((uint64_t)my_row * cache.n_heads + h) * b.max_pages;
-
-  const bool live = c * 8 < hd;
-  const T* base = bounds + (uint64_t)h * 2 * hd + c * 8;
+  const uint32_t i = min(col >> padded_log2, (uint32_t)n_i - 1), g = col & ((1u << padded_log2) - 1);
+  const T* qrow = (const T*)q.p + (uint64_t)((uint32_t)(sq.row0 + i0) + i) * q.token_stride;
+  const T* base = bounds + (uint64_t)h * 2 * hd;
+  const T* zeros = (const T*)zero_row;
+  const int32_t* table = b.table + (uint64_t)s * b.table_stride;
   const uint64_t page_size = (uint64_t)cache.n_heads * 2 * hd;
-  const int steps = (hi_p - p0 + PP - 1) / PP;
+  const bool writes = g == 0 && (col >> padded_log2) < (uint32_t)n_i;
+  const uint64_t item = (uint64_t)((uint32_t)(sq.row0 + i0) + i) * cache.n_heads + h;
 
-  for (uint32_t v0 = 0; v0 < group; v0 += kVecs) {  // one pass unless a row has more than four
-    const uint32_t nv = min((uint32_t)kVecs, group * (uint32_t)n_i - v0);
-    double x[kVecs][8];
+  v8 qp[KS], qn[KS], qm[KS];  // q+, q-, -q-
+  auto load_q = [&](uint32_t v0) {
+    const uint32_t e = v0 + g < group ? v0 + g : 0;  // padding: a head twice
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const uint32_t m = v0 + v;
-      v8 y = {};
-      if ((uint32_t)v < nv && live)
-        y = load_row8((const T*)q.p + (uint64_t)((uint32_t)(sq.row0 + i0) + m / group) * q.token_stride +
-                      (uint64_t)(h * group + m % group) * q.head_stride + c * 8);
+    for (int k = 0; k < KS; ++k) {
+      const uint32_t c = (k * 4 + quarter) * 8;
+      const v8 x = load_row8(c < hd ? qrow + (uint64_t)(h * group + e) * q.head_stride + c : zeros);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[v][e] = (double)to_f32(y[e]);
-    }
-    v8 lo[kAhead], hi[kAhead];
-    auto load = [&](int step, v8& a, v8& d) {
-      const int32_t pid = __shfl(id, (step * PP + (int)sub) % kWave);
-      const T* at = pid >= 0 && live ? base + (uint64_t)(uint32_t)pid * page_size : (const T*)zero_row;
-      a = load_row8(at);
-      d = load_row8(pid >= 0 && live ? at + hd : at);
-    };
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) load(a, lo[a], hi[a]);
-    for (int step0 = 0; step0 < steps; step0 += kAhead) {
-#pragma unroll
-      for (int ah = 0; ah < kAhead; ++ah) {
-        const int step = step0 + ah;
-        if (step >= steps) break;
-        const v8 la = lo[ah], ha = hi[ah];
-        load(step + kAhead, lo[ah], hi[ah]);
-        double a[kVecs];
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) a[v] = 0.0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const double y = (double)to_f32(la[e]), z = (double)to_f32(ha[e]);
-          const double m = z + y, r = z - y;
-#pragma unroll
-          for (int v = 0; v < kVecs; ++v) a[v] = fma(x[v][e], m, fma(fabs(x[v][e]), r, a[v]));
-        }
-        // lanes with bit LP/2 keep vectors 2, 3; of those, lanes with bit LP/4 the odd one
-        auto fold = [&]() {
-          const bool up = (lane & (LP / 2)) != 0, odd = (lane & (LP / 4)) != 0;
-          const double k0 = (up ? a[2] : a[0]) + xor_lane<LP / 2>(up ? a[0] : a[2]);
-          const double k1 = (up ? a[3] : a[1]) + xor_lane<LP / 2>(up ? a[1] : a[3]);
-          double r = (odd ? k1 : k0) + xor_lane<LP / 4>(odd ? k0 : k1);
-          if constexpr (LP >= 32) r += xor_lane<4>(r);
-          if constexpr (LP >= 16) r += xor_lane<2>(r);
-          r += xor_lane<1>(r);
-          return r * 0.5;
-        };
-        double r = fold();
-        if (__any(!isfinite(r))) {
-#pragma unroll
-          for (int v = 0; v < kVecs; ++v) {
-            a[v] = 0.0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              a[v] += 2.0 * nan_max64(x[v][e] * (double)to_f32(la[e]), x[v][e] * (double)to_f32(ha[e]));
-          }
-          r = fold();
-        }
-        if (vi >= nv) r = -INFINITY;
-        if (group >= 2) r = nan_max64(r, xor_lane<LP / 4>(r));
-        if (group >= 3) r = nan_max64(r, xor_lane<LP / 2>(r));
-        const int32_t page = p0 + step * PP + (int32_t)sub;
-        const int32_t pid = __shfl(id, step * PP + (int)sub);
-        if (page >= own.lo && page < own.hi) {
-          uint64_t key = score_key(pid >= 0 ? r : -INFINITY);
-          if (v0) {  // this lane wrote it in the pass before
-            const uint64_t was = my_keys[page];
-            key = key > was ? key : was;
-          }
-          my_keys[page] = key;
-        }
+      for (int r = 0; r < 8; ++r) {
+        const bool neg = to_f32(x[r]) < 0.f;  // a NaN stays in q+
+        qp[k][r] = neg ? (T)0.f : x[r];
+        qn[k][r] = neg ? x[r] : (T)0.f;
+        qm[k][r] = neg ? -x[r] : (T)0.f;
       }
     }
+  };
+  auto absolute = [](v8 x) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(v8, __builtin_bit_cast(u32x4, x) & 0x7FFF7FFFu);
+  };
+  // ids of the wave's pages first (lane = page), then two sets of 16 pages' bounds in flight
+  int32_t id = p0 + (int32_t)lane;
+  id = (int32_t)lane < kPages && id >= rg.lo && id < rg.hi ? table[id] : -1;
+  const bool bounded = id >= 0 && (uint32_t)id < n_bounds;
+  const uint64_t all_there = __ballot(bounded);
+  v8 lo[2][KS], hi[2][KS];
+  auto load = [&](int a) {
+    const int from = a * 16 + (int)col;
+    const int32_t pid = __shfl(id, from);
+    const bool has = (all_there >> from) & 1u;
+    const T* at = has ? base + (uint64_t)(uint32_t)pid * page_size : zeros;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const uint32_t c = (k * 4 + quarter) * 8;
+      lo[a % 2][k] = load_row8(c < hd ? at + c : zeros);
+      hi[a % 2][k] = load_row8(c < hd ? (has ? at + hd : at) + c : zeros);
+    }
+  };
+  load(0);
+  load_q(0);
+  float most = 0.f;
+#pragma unroll
+  for (int a = 0; a < kPages / 16; ++a) {
+    if (a + 1 < kPages / 16) load(a + 1);
+    const uint32_t there = (uint32_t)(all_there >> (16 * a));
+    f32x4 sc, mag;
+    for (uint32_t v0 = 0; v0 < group; v0 += 16) {  // one pass up to 16 heads a group
+      if (group > 16) load_q(v0);
+      f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f}, m = x;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        x = mfma16(hi[a % 2][k], qp[k], x);
+        m = mfma16(absolute(hi[a % 2][k]), qp[k], m);
+        x = mfma16(lo[a % 2][k], qn[k], x);
+        m = mfma16(absolute(lo[a % 2][k]), qm[k], m);
+      }
+      settle(x, m);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        // anything that is no number makes the magnitude infinite, and all scores are formed anew
+        const float y = m[r] == m[r] && x[r] == x[r] ? m[r] : INFINITY;
+        sc[r] = v0 ? fmaxf(sc[r], x[r]) : x[r];
+        mag[r] = v0 ? fmaxf(mag[r], y) : y;
+      }
+    }
+    // the largest over a row's vectors, in neighbouring columns
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (padded_log2 > 0) sc[r] = max_lane<1>(sc[r]), mag[r] = max_lane<1>(mag[r]);
+      if (padded_log2 > 1) sc[r] = max_lane<2>(sc[r]), mag[r] = max_lane<2>(mag[r]);
+      if (padded_log2 > 2) sc[r] = max_lane<4>(sc[r]), mag[r] = max_lane<4>(mag[r]);
+      if (padded_log2 > 3) sc[r] = max_lane<8>(sc[r]), mag[r] = max_lane<8>(mag[r]);
+      most = fmaxf(most, mag[r]);
+      if (!((there >> (4 * quarter + r)) & 1u)) sc[r] = -INFINITY;
+    }
+    if (writes) *(f32x4*)(out.s + item * out.pages + p0 + a * 16 + 4 * quarter) = sc;
   }
+  most = max_half(max_quarter(most));
+  if (writes && quarter == 0) out.mag[item * (out.pages / kPages) + p0 / kPages] = most;
 }
 
-// A workgroup per (row, key head): the smallest key taken, found digit by digit
-// (histograms of the candidates that agree so far), then the pages in order.  The
-// keys are counted from the smallest one, so that the first digit already
-// spreads them over its bins.
+// A page's score as the definition has it, in 64 bits, by a wave: 2^lp_log2 lanes a head,
+// eight channels each, as many heads at a time as that makes.  The order of the sum is the
+// same for every page, so equal bounds have equal scores.
+template <typename T>
+__device__ __forceinline__ double exact_score(const T* __restrict__ lo, const T* q, uint64_t head_stride,
+                                              uint32_t group, uint32_t hd, uint32_t lp_log2,
+                                              uint32_t lane) {
+  const uint32_t c = (lane & ((1u << lp_log2) - 1)) * 8, sub = lane >> lp_log2;
+  const bool live = c < hd;
+  const V8<T> l = load_row8(live ? lo + c : (const T*)zero_row);
+  const V8<T> u = load_row8(live ? lo + hd + c : (const T*)zero_row);
+  double best = -INFINITY;
+  for (uint32_t g0 = 0; g0 < group; g0 += (uint32_t)kWave >> lp_log2) {
+    const bool on = g0 + sub < group;
+    const V8<T> x = load_row8(live && on ? q + (g0 + sub) * head_stride + c : (const T*)zero_row);
+    double sum = 0.0;
+    if (live && on)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const double y = (double)to_f32(x[e]);
+        sum += nan_max64(y * (double)to_f32(l[e]), y * (double)to_f32(u[e]));
+      }
+    for (uint32_t d = 1; d < 1u << lp_log2; d <<= 1) sum += __shfl_xor(sum, (int)d, kWave);
+    if (on) best = nan_max64(best, sum);
+  }
+  for (uint32_t d = 1u << lp_log2; d < (uint32_t)kWave; d <<= 1)
+    best = nan_max64(best, __shfl_xor(best, (int)d, kWave));
+  return best;
+}
+
+// Order-preserving image of a 32-bit score (none is a NaN here).
+__device__ __forceinline__ uint32_t score_key32(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u >> 31) ? ~u : (u | 0x80000000u);
+}
+
+// A workgroup per (row, key head).  The 32-bit scores are off by at most E = 2^-13 of the
+// largest sum of magnitudes (up to 16 products of 32 terms, each of whose additions rounds,
+// or cuts, to 2^-23: 2^-14) plus what a flushed result could be.  With T the need-th
+// largest of them, the need-th largest exact score lies within E of T, so a page
+// more than 2 E above T is taken and one more than 2 E below is not; the few between are
+// scored exactly and the best of them taken.  Selections are digit searches: histograms
+// of the candidates that agree in the digits so far, counted from the smallest one, so that
+// the first digit already spreads them over its bins.
+constexpr uint32_t kCachedPages = 12288;  // whose scores LDS holds (48 KB beside 9)
+constexpr uint32_t kOpen = 256;            // open pages that are ranked one by one
 constexpr uint32_t kDigit = 11, kBins = 1u << kDigit;
 
-template <int NT>
-__global__ __launch_bounds__(NT) void k_kv_pick(Cache cache, Batch b, uint32_t n_first,
-                                                uint32_t n_last, uint32_t n_select,
-                                                const uint64_t* __restrict__ keys,
+template <typename T, int NT, bool kCached>
+__global__ __launch_bounds__(NT) void k_kv_pick(Cache cache, Batch b, const T* __restrict__ bounds,
+                                                uint32_t n_bounds, Rows q, uint32_t n_first,
+                                                uint32_t n_last, uint32_t n_select, Scores in,
                                                 int32_t* __restrict__ sel) {
   constexpr int NW = NT / kWave;
   constexpr int BPT = kBins / NT;  // bins of a thread
@@ -224,8 +254,12 @@ __global__ __launch_bounds__(NT) void k_kv_pick(Cache cache, Batch b, uint32_t n
   __shared__ uint64_t s_lo[NW], s_hi[NW];
   __shared__ uint32_t s_digit, s_need, s_count;
   __shared__ uint32_t s_wave[2][NW];
+  __shared__ uint32_t s_open;
+  __shared__ uint64_t s_key[kOpen];
+  __shared__ int32_t s_page[kOpen];
+  extern __shared__ float s_cached[];  // kCached: the scores of pages rg.lo ..
   const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const uint32_t r = blockIdx.x / cache.n_heads;
+  const uint32_t r = blockIdx.x / cache.n_heads, h = blockIdx.x % cache.n_heads;
   const int32_t s = seq_of_row(b, (int32_t)r);
   if (s < 0) return;
   const Seq sq = load_seq(b, s);
@@ -237,81 +271,203 @@ __global__ __launch_bounds__(NT) void k_kv_pick(Cache cache, Batch b, uint32_t n
     for (uint32_t e = tid; e < n_select; e += NT) list[e] = (int32_t)e <= rg.last ? (int32_t)e : -1;
     return;
   }
-  const uint64_t* mine = keys + (uint64_t)blockIdx.x * b.max_pages;
+  float* score = in.s + (uint64_t)blockIdx.x * in.pages;
+  const float* mags = in.mag + (uint64_t)blockIdx.x * (in.pages / kPages);
+  uint64_t* exact = in.exact + (uint64_t)blockIdx.x * in.pages;
   for (uint32_t e = tid; e < n_first; e += NT) list[e] = (int32_t)e;
   for (uint32_t e = tid; e < n_last; e += NT)
     list[n_select - n_last + e] = rg.last + 1 - (int32_t)n_last + (int32_t)e;
   uint32_t need = n_select - n_first - n_last;  // < hi - lo, since last + 1 > n_select
   if (need == 0) return;
 
-  uint64_t lo = ~0ull, hi = 0;
+  // the smallest and largest of all threads' lo and hi, to all threads
+  auto spread = [&](uint64_t& lo, uint64_t& hi) {
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const uint64_t x = (uint64_t)__shfl_xor((long long)lo, d), y = (uint64_t)__shfl_xor((long long)hi, d);
+      lo = x < lo ? x : lo;
+      hi = y > hi ? y : hi;
+    }
+    __syncthreads();
+    if (lane == 0) {
+      s_lo[wave] = lo;
+      s_hi[wave] = hi;
+    }
+    __syncthreads();
+    for (int w = 0; w < NW; ++w) {
+      lo = s_lo[w] < lo ? s_lo[w] : lo;
+      hi = s_hi[w] > hi ? s_hi[w] : hi;
+    }
+  };
+  // The n-th largest of key(p) - lo where among(p), all of them below hi - lo + 1, down to a
+  // digit where the candidates that agree are all taken, or are no more than `few`:
+  // candidates whose bits from `shift` up are above `prefix` are taken, and n of those equal.
+  auto search = [&](auto&& among, auto&& key, uint64_t lo, uint64_t hi, uint32_t few, uint32_t& n,
+                    int& shift, uint64_t& prefix) {
+    shift = hi == lo ? 0 : 64 - __clzll((long long)(hi - lo));
+    prefix = 0;
+    bool all = false;
+    while (shift > 0 && !all) {
+      const int width = shift < (int)kDigit ? shift : (int)kDigit;
+      const int next = shift - width;
+#pragma unroll
+      for (int e = 0; e < BPT; ++e) hist[tid * BPT + e] = 0;
+      __syncthreads();
+      for (int32_t p = rg.lo + (int32_t)tid; p < rg.hi; p += NT) {
+        if (!among(p)) continue;
+        const uint64_t k = key(p) - lo;
+        if (shift == 64 || (k >> shift) == prefix)
+          atomicAdd(&hist[(uint32_t)(k >> next) & ((1u << width) - 1u)], 1u);
+      }
+      __syncthreads();
+      // the bin in which the n-th candidate from the top lies: counts above each thread's bins
+      uint32_t own[BPT], sum = 0;
+#pragma unroll
+      for (int e = 0; e < BPT; ++e) sum += own[e] = hist[kBins - 1 - (tid * BPT + e)];
+      const uint32_t incl = wave_inclusive_sum(sum);
+      if (lane == kWave - 1) s_wave[0][wave] = incl;
+      __syncthreads();
+      uint32_t above = incl - sum;
+      for (uint32_t w = 0; w < wave; ++w) above += s_wave[0][w];
+#pragma unroll
+      for (int e = 0; e < BPT; ++e) {
+        if (above < n && n <= above + own[e]) {
+          s_digit = kBins - 1 - (tid * BPT + e);
+          s_need = n - above;
+          s_count = own[e];
+        }
+        above += own[e];
+      }
+      __syncthreads();
+      prefix = (prefix << width) | s_digit;
+      n = s_need;
+      all = s_count == n || s_count <= few;
+      shift = next;
+      __syncthreads();
+    }
+  };
+
+  uint64_t lo32 = ~0ull, hi32 = 0;  // of the 32-bit scores' images
   for (int32_t p = rg.lo + (int32_t)tid; p < rg.hi; p += NT) {
-    const uint64_t k = mine[p];
-    lo = k < lo ? k : lo;
-    hi = k > hi ? k : hi;
+    const float x = score[p];
+    if (kCached) s_cached[p - rg.lo] = x;
+    const uint64_t k = score_key32(x);
+    lo32 = k < lo32 ? k : lo32;
+    hi32 = k > hi32 ? k : hi32;
+  }
+  auto score_of = [&](int32_t p) { return kCached ? s_cached[p - rg.lo] : score[p]; };
+  spread(lo32, hi32);
+
+  // E, and the border of the 32-bit scores, or rather two values that it lies between: the ends
+  // of a bin that holds few of them
+  float mag = 0.f;
+  for (int32_t e = rg.lo / kPages + (int32_t)tid; e <= (rg.hi - 1) / kPages; e += NT)
+    mag = fmaxf(mag, mags[e]);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) mag = fmaxf(mag, __shfl_xor(mag, d, kWave));
+  if (lane == 0) s_wave[0][wave] = __float_as_uint(mag);
+  __syncthreads();
+  for (int w = 0; w < NW; ++w) mag = fmaxf(mag, __uint_as_float(s_wave[0][w]));
+  const bool numbers = mag < 1e38f;  // (a sum near the largest number may have passed it)
+  float sure = INFINITY, maybe = -INFINITY;  // above `sure`: taken; from `maybe` up: perhaps
+  if (numbers) {
+    uint64_t prefix;
+    uint32_t n = need;
+    int shift;
+    search([](int32_t) { return true; }, [&](int32_t p) { return (uint64_t)score_key32(score_of(p)); },
+           lo32, hi32, 8, n, shift, prefix);
+    auto value = [](uint64_t k) {
+      return __uint_as_float((uint32_t)k >> 31 ? (uint32_t)k & 0x7FFFFFFFu : ~(uint32_t)k);
+    };
+    const uint64_t first = lo32 + (prefix << shift), last = lo32 + ((prefix + 1) << shift) - 1;
+    const float e2 = 2.f * (mag * 0x1p-13f + 0x1p-100f);
+    sure = value(last < hi32 ? last : hi32) + e2;
+    maybe = value(first) - e2;
+  }
+  auto taken = [&](int32_t p) { return numbers && score_of(p) > sure; };
+  auto open = [&](int32_t p) { return !numbers || (score_of(p) >= maybe && score_of(p) <= sure); };
+  if (tid == 0) s_open = 0;
+  __syncthreads();
+  uint32_t n_taken = 0;
+  for (int32_t p = rg.lo + (int32_t)tid; p < rg.hi; p += NT) {
+    n_taken += taken(p);
+    if (open(p)) {
+      const uint32_t e = atomicAdd(&s_open, 1u);
+      if (e < kOpen) s_page[e] = p;
+    }
   }
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const uint64_t a = (uint64_t)__shfl_xor((long long)lo, d), e = (uint64_t)__shfl_xor((long long)hi, d);
-    lo = a < lo ? a : lo;
-    hi = e > hi ? e : hi;
-  }
-  if (lane == 0) {
-    s_lo[wave] = lo;
-    s_hi[wave] = hi;
+  for (int d = 1; d < kWave; d <<= 1) n_taken += __shfl_xor(n_taken, d, kWave);
+  if (lane == 0) s_wave[0][wave] = n_taken;
+  __syncthreads();
+  n_taken = 0;
+  for (int w = 0; w < NW; ++w) n_taken += s_wave[0][w];
+  const uint32_t n_open = s_open;
+  need -= n_taken;  // of the open ones; at least one, the border itself
+  const uint32_t group = q.n_heads / cache.n_heads, hd = cache.head_dim;
+  const uint32_t lp_log2 = hd <= 64 ? 3 : hd <= 128 ? 4 : 5;
+  const T* qrow = (const T*)q.p + r * q.token_stride + (uint64_t)h * group * q.head_stride;
+  const int32_t* table = b.table + (uint64_t)s * b.table_stride;
+  auto exact_key = [&](int32_t p) {
+    const int32_t id = table[p];
+    double x = -INFINITY;
+    if (id >= 0 && (uint32_t)id < n_bounds)
+      x = exact_score(bounds + ((uint64_t)(uint32_t)id * cache.n_heads + h) * 2 * hd, qrow,
+                      q.head_stride, group, hd, lp_log2, lane);
+    return score_key(x);
+  };
+  int shift = 64;   // (64: all open ones are taken)
+  uint64_t prefix = 0, lo = 0, hi = 0;
+  bool listed = false;  // whether the open ones' 32-bit scores now say if they are taken
+  if (n_open > need && n_open <= kOpen) {
+    // few: each one's rank among them
+    for (uint32_t e = wave; e < n_open; e += NW) {
+      const uint64_t k = exact_key(s_page[e]);
+      if (lane == 0) s_key[e] = k;
+    }
+    __syncthreads();
+    if (tid < n_open) {
+      const uint64_t k = s_key[tid];
+      const int32_t p = s_page[tid];
+      uint32_t rank = 0;
+      for (uint32_t e = 0; e < n_open; ++e) rank += s_key[e] > k || (s_key[e] == k && s_page[e] < p);
+      const float x = rank < need ? INFINITY : -INFINITY;
+      if (kCached) s_cached[p - rg.lo] = x;
+      else score[p] = x;
+    }
+    listed = true;
+  } else if (n_open > need) {
+    for (int32_t base = rg.lo + (int32_t)wave * kWave; base < rg.hi; base += NT) {
+      const int32_t p = base + (int32_t)lane;
+      for (uint64_t left = __ballot(p < rg.hi && open(p)); left; left &= left - 1) {
+        const int32_t at = base + __builtin_ctzll(left);
+        const uint64_t k = exact_key(at);
+        if (lane == 0) exact[at] = k;
+      }
+    }
+    __syncthreads();
+    lo = ~0ull;
+    for (int32_t p = rg.lo + (int32_t)tid; p < rg.hi; p += NT) {
+      if (!open(p)) continue;
+      const uint64_t k = exact[p];
+      lo = k < lo ? k : lo;
+      hi = k > hi ? k : hi;
+    }
+    spread(lo, hi);
+    search(open, [&](int32_t p) { return exact[p]; }, lo, hi, 0, need, shift, prefix);
   }
   __syncthreads();
-  for (int w = 0; w < NW; ++w) {
-    lo = s_lo[w] < lo ? s_lo[w] : lo;
-    hi = s_hi[w] > hi ? s_hi[w] : hi;
-  }
-  // keys less lo: `bits` bits; candidates: those whose bits from `shift` up equal `prefix`
-  int shift = hi == lo ? 0 : 64 - __clzll((long long)(hi - lo));
-  uint64_t prefix = 0;
-  bool all = false;  // all candidates are taken
-  while (shift > 0 && !all) {
-    const int width = shift < (int)kDigit ? shift : (int)kDigit;
-    const int next = shift - width;
-#pragma unroll
-    for (int e = 0; e < BPT; ++e) hist[tid * BPT + e] = 0;
-    __syncthreads();
-    for (int32_t p = rg.lo + (int32_t)tid; p < rg.hi; p += NT) {
-      const uint64_t k = mine[p] - lo;
-      if (shift == 64 || (k >> shift) == prefix)
-        atomicAdd(&hist[(uint32_t)(k >> next) & ((1u << width) - 1u)], 1u);
-    }
-    __syncthreads();
-    // the bin in which the need-th candidate from the top lies: counts above each thread's bins
-    uint32_t own[BPT], sum = 0;
-#pragma unroll
-    for (int e = 0; e < BPT; ++e) sum += own[e] = hist[kBins - 1 - (tid * BPT + e)];
-    const uint32_t incl = wave_inclusive_sum(sum);
-    if (lane == kWave - 1) s_wave[0][wave] = incl;
-    __syncthreads();
-    uint32_t above = incl - sum;
-    for (uint32_t w = 0; w < wave; ++w) above += s_wave[0][w];
-#pragma unroll
-    for (int e = 0; e < BPT; ++e) {
-      if (above < need && need <= above + own[e]) {
-        s_digit = kBins - 1 - (tid * BPT + e);
-        s_need = need - above;
-        s_count = own[e];
-      }
-      above += own[e];
-    }
-    __syncthreads();
-    prefix = (prefix << width) | s_digit;
-    need = s_need;
-    all = s_count == need;
-    shift = next;
-  }
-  // candidates above the prefix, and the first `need` that equal it
+  // the taken, the open ones above the prefix, and the first `need` that equal it
   uint32_t out = n_first, equal_before = 0;
   for (int32_t base = rg.lo; base < rg.hi; base += NT) {
     const int32_t p = base + (int32_t)tid;
-    const uint64_t k = p < rg.hi ? mine[p] - lo : 0;
-    const uint64_t top = shift == 64 ? 0 : k >> shift;
-    const bool above = p < rg.hi && top > prefix, equal = p < rg.hi && top == prefix;
+    bool above = p < rg.hi && (taken(p) || (listed && score_of(p) == INFINITY));
+    bool equal = p < rg.hi && !listed && open(p);
+    if (equal && shift < 64) {
+      const uint64_t top = (exact[p] - lo) >> shift;
+      above = top > prefix;
+      equal = top == prefix;
+    }
     const uint64_t be = __ballot(equal), ba = __ballot(above);
     if (lane == 0) {
       s_wave[0][wave] = (uint32_t)__popcll(be);
@@ -330,50 +486,61 @@ __global__ __launch_bounds__(NT) void k_kv_pick(Cache cache, Batch b, uint32_t n
       eq_all += s_wave[0][w];
       ab_all += s_wave[1][w];
     }
-    const uint32_t taken = min(eq, need) - min(equal_before, need);
-    if (above || (equal && eq < need)) list[out + ab + taken] = p;
+    const uint32_t before = min(eq, need) - min(equal_before, need);
+    if (above || (equal && eq < need)) list[out + ab + before] = p;
     out += ab_all + min(eq_all, need) - min(equal_before, need);
     equal_before = eq_all;
     __syncthreads();
   }
 }
 
+uint32_t padded_pages(const Batch& b) {
+  return (b.max_pages + kScorePages - 1) / kScorePages * kScorePages;
+}
+
 template <typename T>
 hipError_t run_select(const Cache& c, const Batch& b, const void* bounds, uint32_t n_bounds,
                       const Rows& q, uint32_t n_first, uint32_t n_last, uint32_t n_select,
-                      int32_t* sel, uint64_t* keys, hipStream_t s) {
+                      int32_t* sel, void* workspace, hipStream_t s) {
   const uint32_t items = b.n_rows * c.n_heads;
+  Scores sc = {nullptr, nullptr, nullptr, padded_pages(b)};
   if (b.max_pages > n_select) {
+    sc.exact = (uint64_t*)workspace;
+    sc.s = (float*)(sc.exact + (uint64_t)items * sc.pages);
+    sc.mag = sc.s + (uint64_t)items * sc.pages;
     const uint32_t group = q.n_heads / c.n_heads;
-    const uint32_t rows = group >= 3 ? 1 : kVecs / group;
+    uint32_t padded_log2 = 0;
+    while ((1u << padded_log2) < group && padded_log2 < 4) ++padded_log2;
+    const uint32_t rows = 16u >> padded_log2;
     const uint32_t tiles = (b.max_q + rows - 1) / rows;
-    const uint32_t page_blocks = (b.max_pages + kScorePages - 1) / kScorePages;
-    const uint64_t blocks = (uint64_t)b.n_seqs * tiles * page_blocks * c.n_heads;
+    const uint64_t blocks = (uint64_t)b.n_seqs * tiles * (sc.pages / kScorePages) * c.n_heads;
     if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
-#define IBP_KV_SCORE(LP)                                                                           \
-  hipLaunchKernelGGL((k_kv_score<T, LP>), dim3((uint32_t)blocks), dim3(256), 0, s, c, b,           \
-                     (const T*)bounds, n_bounds, q, n_first, n_last, n_select, tiles, rows,        \
-                     page_blocks, keys)
-    if (c.head_dim <= 64) IBP_KV_SCORE(8);
-    else if (c.head_dim <= 128) IBP_KV_SCORE(16);
-    else IBP_KV_SCORE(32);
+#define IBP_KV_SCORE(DP)                                                                            \
+  hipLaunchKernelGGL((k_kv_score<T, DP>), dim3((uint32_t)blocks), dim3(256), 0, s, c, b,            \
+                     (const T*)bounds, n_bounds, q, n_first, n_last, n_select, tiles, padded_log2, sc)
+    if (c.head_dim <= 64) IBP_KV_SCORE(64);
+    else if (c.head_dim <= 128) IBP_KV_SCORE(128);
+    else IBP_KV_SCORE(256);
 #undef IBP_KV_SCORE
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (b.max_pages <= 1024)
-    hipLaunchKernelGGL(k_kv_pick<256>, dim3(items), dim3(256), 0, s, c, b, n_first, n_last, n_select,
-                       keys, sel);
-  else
-    hipLaunchKernelGGL(k_kv_pick<1024>, dim3(items), dim3(1024), 0, s, c, b, n_first, n_last,
-                       n_select, keys, sel);
+#define IBP_KV_PICK(NT, CACHED)                                                                    \
+  hipLaunchKernelGGL((k_kv_pick<T, NT, CACHED>), dim3(items), dim3(NT), CACHED ? b.max_pages * 4 : 0, \
+                     s, c, b, (const T*)bounds, n_bounds, q, n_first, n_last, n_select, sc, sel)
+  if (b.max_pages <= 1024) IBP_KV_PICK(256, true);
+  else if (b.max_pages <= kCachedPages) IBP_KV_PICK(1024, true);
+  else IBP_KV_PICK(1024, false);
+#undef IBP_KV_PICK
   return hipGetLastError();
 }
 
 }  // namespace
 
 uint64_t select_workspace(const Cache& c, const Batch& b, uint32_t n_select) {
-  return b.max_pages > n_select ? (uint64_t)b.n_rows * c.n_heads * b.max_pages * 8 : 0;
+  if (b.max_pages <= n_select) return 0;
+  const uint64_t pages = padded_pages(b);
+  return (uint64_t)b.n_rows * c.n_heads * (pages * 12 + pages / kPages * 4);
 }
 
 hipError_t launch_select(const Cache& c, uint32_t dtype, const Batch& b, const void* bounds,
@@ -382,9 +549,9 @@ hipError_t launch_select(const Cache& c, uint32_t dtype, const Batch& b, const v
   if (b.n_rows == 0 || b.n_seqs == 0 || b.max_q == 0) return hipSuccess;
   return dtype == IBP_KV_F16
              ? run_select<_Float16>(c, b, bounds, n_bounds, q, n_first, n_last, n_select, sel,
-                                    (uint64_t*)workspace, s)
+                                    workspace, s)
              : run_select<__bf16>(c, b, bounds, n_bounds, q, n_first, n_last, n_select, sel,
-                                  (uint64_t*)workspace, s);
+                                  workspace, s);
 }
 
 }  // namespace kv

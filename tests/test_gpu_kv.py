@@ -329,6 +329,52 @@ def test_select_ties_and_odd_scores():
         assert torch.equal(sel.cpu(), K.select(c, bounds, 1, 1, n_select)), n_select
 
 
+@pytest.mark.parametrize("n_pages,n_select", [(1000, 40), (1500, 700), (4100, 128), (13000, 500)])
+def test_select_many_pages(n_pages, n_select):
+    """Long lists: pages whose scores differ, pages in large groups of equal bounds (more open
+    ones than are ranked one by one), and scores that differ by less than 32 bits hold."""
+    for kind in ("random", "groups", "close"):
+        page, d = 1, 32
+        c = K.Case([(1, n_pages)], dtype=BF16, d=d, h=2, group=2, page=page, extra=0, seed=n_pages)
+        g = torch.Generator().manual_seed(n_pages)
+        a, b = torch.randn((2, n_pages, 2, d), generator=g)
+        if kind == "groups":  # every 400 pages share their bounds
+            a, b = (x[torch.arange(n_pages) % -(-n_pages // 400)] for x in (a, b))
+        if kind == "close":  # one large channel hides the others from 32-bit sums
+            a = a * 2.0 ** -14
+            b = b * 2.0 ** -14
+            a[..., 0] = b[..., 0] = 300.0
+            c.q[..., 0] = 200.0
+        bounds = torch.zeros((c.n_pages, 2, 2, d), dtype=BF16)
+        ids = c.table[0, :n_pages].long()
+        bounds[ids, :, 0], bounds[ids, :, 1] = torch.minimum(a, b).to(BF16), torch.maximum(a, b).to(BF16)
+        c.table[0, 5] = -1
+        k, v = c.pools()
+        cache, batch = kv.Cache(k, v), gpu_batch(c)
+        sel = torch.full((1, 2, n_select), -7, dtype=torch.int32, device="cuda")
+        log(f"many pages {n_pages} {n_select} {kind}")
+        kv.select(cache, batch, bounds.cuda(), c.wide_q.cuda()[:, :4], sel, n_first=2, n_last=3,
+                  workspace=ws(kv.select_workspace(cache, batch, 1, n_select)))
+        assert torch.equal(sel.cpu(), K.select(c, bounds, 2, 3, n_select)), kind
+
+
+@pytest.mark.parametrize("group", [17, 40])
+def test_select_large_groups(group):
+    """More query heads a key head than one product holds."""
+    c = K.Case([(1, 700), (2, 301)], dtype=F16, d=64, h=1, group=group, page=8)
+    bounds = K.all_bounds(c)
+    k, v = c.pools()
+    cache, batch = kv.Cache(k, v), gpu_batch(c)
+    sel = torch.full((c.n, 1, 12), -7, dtype=torch.int32, device="cuda")
+    log(f"large group {group}")
+    kv.select(cache, batch, bounds.cuda(), c.wide_q.cuda()[:, :group], sel, n_first=1, n_last=2,
+              workspace=ws(kv.select_workspace(cache, batch, c.n, 12)))
+    want = K.select(c, bounds, 1, 2, 12)
+    assert torch.equal(sel.cpu(), want)
+    out, lse = run_attend(c, 0.1, sel=want)
+    K.check_attention(c, out, lse, K.attention(c, 0.1, sel=want), "large group")
+
+
 def test_attend_selected_lists():
     """Lists with repeats, pages past the sequence, gaps and nothing at all."""
     c = K.Case([(1, 100), (3, 260), (1, 90)], d=64, h=2, group=3, page=16, fill=math.nan)
