@@ -7,8 +7,20 @@ namespace kv {
 
 namespace {
 
+// How a call is run.
+//   few    Up to 16 rows share a sequence's keys (one new token, or a few, with its group of
+//          heads), or each row has its own list of pages.
+//   heads  Four key heads to a workgroup where their number allows: its waves then read
+//          neighbouring parts of the same token rows (OPT-13B decode 172 -> 162 us), instead of
+//          different keys of one head.
+//   splits The keys of a row tile over several workgroups until the GPU has eight (few) or two
+//          a CU: more than it runs at a time, so that the last ones to finish are short (few: 4
+//          a CU 175 / 340 us, 8 172 / 314, 12 166 / 320 for OPT-13B decode / 131072-token
+//          contexts), but no split below 256 keys of a wave's turn (few) or 512.
+// A window bounds the keys of a tile; the workspace is sized without one, for as many splits or
+// more.
 hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
-                     AttendPlan* p) {
+                     uint32_t window, AttendPlan* p) {
   DeviceInfo di;
   hipError_t e = device_info(&di);
   if (e != hipSuccess) return e;
@@ -17,11 +29,14 @@ hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_
   p->few = n_select || rows <= 16;
   const uint64_t tile = p->few ? 16 : kChunkRows;
   p->row_tiles = (uint32_t)((rows + tile - 1) / tile);
-  const uint64_t base = (uint64_t)(n_select ? b.n_rows : b.n_seqs) * p->row_tiles * c.n_heads;
-  const uint64_t keys = n_select ? (uint64_t)n_select * c.page.d : b.max_kv;
-  const uint64_t want = (uint64_t)di.cus * (p->few ? 4 : 2);
+  p->heads = p->few && !n_select && c.n_heads % 4 == 0 ? 4 : 1;
+  const uint64_t base = (uint64_t)(n_select ? b.n_rows : b.n_seqs) * p->row_tiles * (c.n_heads / p->heads);
+  uint64_t keys = n_select ? (uint64_t)n_select * c.page.d : b.max_kv;
+  if (window && keys > (uint64_t)window + b.max_q) keys = (uint64_t)window + b.max_q;
+  const uint64_t want = (uint64_t)di.cus * (p->few ? 8 : 2);
   uint64_t splits = base ? (want + base - 1) / base : 1;
-  if (splits > keys / (p->few ? 256 : 512)) splits = keys / (p->few ? 256 : 512);
+  const uint64_t least = p->few ? 256 / p->heads : 512;  // keys that are worth a split
+  if (splits > keys / least) splits = keys / least;
   if (splits > kMaxSplits) splits = kMaxSplits;
   p->splits = splits < 1 ? 1 : (uint32_t)splits;
   p->blocks = base * p->splits;
@@ -39,7 +54,7 @@ uint64_t partial_bytes(const Cache& c, const Batch& b, uint32_t n_q_heads, const
 hipError_t attend_workspace(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
                             uint64_t* bytes) {
   AttendPlan p;
-  hipError_t e = make_plan(c, b, n_q_heads, n_select, &p);
+  hipError_t e = make_plan(c, b, n_q_heads, n_select, 0, &p);
   if (e == hipSuccess) *bytes = partial_bytes(c, b, n_q_heads, p);
   return e;
 }
@@ -49,7 +64,7 @@ hipError_t launch_attend(const Cache& c, uint32_t dtype, const Batch& b, const R
                          uint32_t window, bool causal, float* lse, void* workspace,
                          hipStream_t s) {
   AttendPlan p;
-  hipError_t e = make_plan(c, b, q.n_heads, n_select, &p);
+  hipError_t e = make_plan(c, b, q.n_heads, n_select, window, &p);
   if (e != hipSuccess) return e;
   Partial part;
   part.splits = p.splits;

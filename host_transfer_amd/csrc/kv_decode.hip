@@ -13,7 +13,6 @@ namespace {
 
 constexpr int kTile = 32;                // keys of a wave's step
 constexpr int kWaves = 4;
-constexpr int kBlockKeys = kTile * kWaves;
 
 // A workgroup per (up to 16 rows that share a key head, split of their keys).
 // Its four waves take 32 keys at a time, in turn, each with a running
@@ -29,7 +28,7 @@ constexpr int kBlockKeys = kTile * kWaves;
 // the transposed read gives the second product's operand.  LDS rows are padded by
 // 32 B: the eight rows that half a wave reads then lie in eight different 32 B
 // windows of the banks for every head_dim that is a multiple of 32.
-template <typename T, int DP, bool kSelected>
+template <typename T, int DP, bool kSelected, int kHeads>
 __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q, Rows out,
                                                    const int32_t* __restrict__ sel,
                                                    uint32_t n_select, float scale_log2,
@@ -41,6 +40,8 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
   constexpr int LD = DP + 16;   // LDS row, elements
   constexpr int WORDS = kTile * LD / 2;  // of a wave; 16 rows of DP floats fit
   static_assert(16 * DP <= WORDS, "the end's exchange fits the V tiles");
+  constexpr int kTurns = kWaves / kHeads;           // waves that share a key head
+  constexpr int kBlockKeys = kTile * kTurns;
   __shared__ __align__(16) uint32_t s_v[kWaves][WORDS];
   __shared__ float s_m[kWaves][16], s_z[kWaves][16];
 
@@ -52,8 +53,9 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
   // block -> (sequence or row, row tile, split, key head), heads innermost: the
   // heads of a token lie side by side in memory
   uint32_t u = blockIdx.x;
-  const uint32_t kh = u % cache.n_heads;
-  u /= cache.n_heads;
+  const uint32_t head_blocks = cache.n_heads / kHeads;
+  const uint32_t kh = u % head_blocks * kHeads + wave % kHeads;
+  u /= head_blocks;
   const uint32_t split = u % part.splits;
   u /= part.splits;
   const uint32_t tile = u % row_tiles;
@@ -154,7 +156,7 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
   const T* tr_at = sv + (4 * quarter + col / 4) * LD + 4 * (col % 4);
   bool odd = false;  // values that only some rows see and that are no numbers were left out
 
-  for (int32_t t0 = begin + (int32_t)wave * kTile; t0 < end; t0 += kBlockKeys) {
+  for (int32_t t0 = begin + (int32_t)(wave / kHeads) * kTile; t0 < end; t0 += kBlockKeys) {
     V8<T> kf[2][KS], vf[2][KS];
     uint32_t there[2];
     bool plain = true;
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
 
   settle(o);
   if (!kSelected && __any(odd)) {
-    for (int32_t t0 = begin + (int32_t)wave * kTile; t0 < end; t0 += kBlockKeys) {
+    for (int32_t t0 = begin + (int32_t)(wave / kHeads) * kTile; t0 < end; t0 += kBlockKeys) {
       if (t0 >= lo_e && t0 + kTile <= hi_a) continue;
       V8<T> sees;
 #pragma unroll
@@ -298,31 +300,33 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
     s_z[wave][col] = z;
   }
   __syncthreads();
-  // 16 threads a row
-  const uint32_t r = threadIdx.x / 16;
+  // a row of a head to 16 / kHeads threads; the head's waves are mine, mine + kHeads, ...
+  constexpr uint32_t kOf = 256 / kHeads, kRowThreads = kOf / 16;
+  const uint32_t mine = threadIdx.x / kOf, r = threadIdx.x % kOf / kRowThreads;
+  const uint32_t first_c = threadIdx.x % kRowThreads;
   if (m0 + r >= m1) return;
-  float mm = s_m[0][r];
+  float mm = s_m[mine][r];
 #pragma unroll
-  for (int a = 1; a < kWaves; ++a) mm = fmaxf(mm, s_m[a][r]);
-  float f[kWaves], zz = 0.f;
+  for (int a = 1; a < kTurns; ++a) mm = fmaxf(mm, s_m[mine + a * kHeads][r]);
+  float f[kTurns], zz = 0.f;
 #pragma unroll
-  for (int a = 0; a < kWaves; ++a) {
-    f[a] = exp2_raw(s_m[a][r] - (mm == -INFINITY ? 0.f : mm));
-    zz += f[a] * s_z[a][r];
+  for (int a = 0; a < kTurns; ++a) {
+    f[a] = exp2_raw(s_m[mine + a * kHeads][r] - (mm == -INFINITY ? 0.f : mm));
+    zz += f[a] * s_z[mine + a * kHeads][r];
   }
   const uint32_t rm = m0 + r;
-  const uint32_t rrow = (uint32_t)(sq.row0 + i0) + rm / group, rhead = kh * group + rm % group;
+  const uint32_t rrow = (uint32_t)(sq.row0 + i0) + rm / group, rhead = (kh - wave % kHeads + mine) * group + rm % group;
   const uint64_t unit = (uint64_t)rrow * q.n_heads + rhead;
   const bool whole = part.splits == 1;
   const float inv = whole ? (zz == 0.f ? 0.f : 1.f / zz) : 1.f;
   T* op = (T*)out.p + rrow * out.token_stride + (uint64_t)rhead * out.head_stride;
-  for (uint32_t c = threadIdx.x % 16; c < hd / 8; c += 16) {
+  for (uint32_t c = first_c; c < hd / 8; c += kRowThreads) {
     float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       y[e] = 0.f;
 #pragma unroll
-      for (int a = 0; a < kWaves; ++a) y[e] += f[a] * ((const float*)s_v[a])[r * DP + c * 8 + e];
+      for (int a = 0; a < kTurns; ++a) y[e] += f[a] * ((const float*)s_v[mine + a * kHeads])[r * DP + c * 8 + e];
       y[e] *= inv;
     }
     if (whole) {
@@ -336,7 +340,7 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
       *(f32x4*)(to_ + 4) = f32x4{y[4], y[5], y[6], y[7]};
     }
   }
-  if (threadIdx.x % 16 == 0) {
+  if (first_c == 0) {
     if (!whole) part.ms[unit * part.splits + split] = make_float2(mm, zz);
     else if (lse) lse[unit] = zz == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(zz)) * kLn2;
   }
@@ -416,11 +420,11 @@ __global__ __launch_bounds__(256) void k_kv_join(Batch b, Rows out, Partial part
   if (lse && tid == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
 }
 
-template <typename T, int DP, bool kSelected>
+template <typename T, int DP, bool kSelected, int kHeads>
 hipError_t run_decode(const AttendPlan& p, const Cache& c, const Batch& b, const Rows& q,
                       const Rows& out, const int32_t* sel, uint32_t n_select, float scale,
                       uint32_t window, bool causal, float* lse, Partial part, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv_decode<T, DP, kSelected>), dim3((uint32_t)p.blocks), dim3(256), 0, s, c,
+  hipLaunchKernelGGL((k_kv_decode<T, DP, kSelected, kHeads>), dim3((uint32_t)p.blocks), dim3(256), 0, s, c,
                      b, q, out, sel, n_select, scale * kLog2e, window, causal, p.row_tiles, part, lse);
   return hipGetLastError();
 }
@@ -431,14 +435,17 @@ hipError_t launch_decode(const AttendPlan& p, const Cache& c, uint32_t dtype, co
                          const Rows& q, const Rows& out, const int32_t* sel, uint32_t n_select,
                          float scale, uint32_t window, bool causal, float* lse, Partial part,
                          hipStream_t s) {
-#define IBP_KV_DECODE(T, DP, SEL) \
-  run_decode<T, DP, SEL>(p, c, b, q, out, sel, n_select, scale, window, causal, lse, part, s)
-#define IBP_KV_DECODE_T(T, SEL)                                          \
-  (c.head_dim <= 64 ? IBP_KV_DECODE(T, 64, SEL)                          \
-                    : c.head_dim <= 128 ? IBP_KV_DECODE(T, 128, SEL) : IBP_KV_DECODE(T, 256, SEL))
-  if (dtype == IBP_KV_F16)
-    return sel ? IBP_KV_DECODE_T(_Float16, true) : IBP_KV_DECODE_T(_Float16, false);
-  return sel ? IBP_KV_DECODE_T(__bf16, true) : IBP_KV_DECODE_T(__bf16, false);
+#define IBP_KV_DECODE(T, DP, SEL, HEADS) \
+  run_decode<T, DP, SEL, HEADS>(p, c, b, q, out, sel, n_select, scale, window, causal, lse, part, s)
+#define IBP_KV_DECODE_T(T, SEL, HEADS)                                          \
+  (c.head_dim <= 64    ? IBP_KV_DECODE(T, 64, SEL, HEADS)                       \
+   : c.head_dim <= 128 ? IBP_KV_DECODE(T, 128, SEL, HEADS)                      \
+                       : IBP_KV_DECODE(T, 256, SEL, HEADS))
+#define IBP_KV_DECODE_S(T)                                                      \
+  (sel            ? IBP_KV_DECODE_T(T, true, 1)                                 \
+   : p.heads == 4 ? IBP_KV_DECODE_T(T, false, 4) : IBP_KV_DECODE_T(T, false, 1))
+  return dtype == IBP_KV_F16 ? IBP_KV_DECODE_S(_Float16) : IBP_KV_DECODE_S(__bf16);
+#undef IBP_KV_DECODE_S
 #undef IBP_KV_DECODE_T
 #undef IBP_KV_DECODE
 }

@@ -164,6 +164,7 @@ constexpr uint32_t kMaxSplits = 1024;
 struct AttendPlan {
   bool few;            // few rows share their keys: kv_decode.hip, else kv_chunk.hip
   uint32_t row_tiles;  // of a sequence and key head (of a row and key head in lists)
+  uint32_t heads;      // key heads of a workgroup of kv_decode.hip
   uint32_t splits;
   uint64_t blocks;
 };
