@@ -11,7 +11,12 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Workgroups of 256 threads a launch takes (its threads are counted in 32 bits).
+constexpr uint64_t kMaxBlocks = 0xFFFFFFull;
+
 int hip_fail(hipError_t e, const char* name) {
+  if (e == hipErrorInvalidConfiguration)
+    return set_error(IBP_ERR_SIZE, "%s: more workgroups than a launch takes", name);
   return set_error(IBP_ERR_HIP, "%s: HIP error %d (%s)", name, (int)e, hipGetErrorString(e));
 }
 
@@ -158,8 +163,8 @@ int check_group(const char* name, const ibp::kv::Cache& c, uint32_t n_q_heads) {
 }
 
 int check_items(const char* name, uint64_t rows, uint64_t heads) {
-  if (rows * heads > 0x7FFFFFFFull)
-    return set_error(IBP_ERR_SIZE, "%s: rows x heads must be below 2^31", name);
+  if (rows * heads > kMaxBlocks)
+    return set_error(IBP_ERR_SIZE, "%s: rows x heads must be below 2^24", name);
   return IBP_OK;
 }
 
@@ -268,7 +273,8 @@ int ibp_kv_append(const ibp_kv_cache* cache, const ibp_kv_rows* k, const ibp_kv_
         (qr.token_stride != qo.token_stride || qr.head_stride != qo.head_stride))
       return set_error(IBP_ERR_SIZE, "%s: q_out in place of q needs q's strides", name);
   }
-  if ((r = check_items(name, n_tokens, (uint64_t)qr.n_heads + 2 * c.n_heads))) return r;
+  if (c.k == c.v)
+    return set_error(IBP_ERR_SIZE, "%s: k and v of the cache are the same memory", name);
   if (rope) {
     if (rope_dim == 0 || rope_dim % 16 != 0 || rope_dim > c.head_dim)
       return set_error(IBP_ERR_SIZE, "%s: rope_dim %u must be a multiple of 16 in [16, head_dim]",

@@ -40,7 +40,7 @@ hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_
   if (splits > kMaxSplits) splits = kMaxSplits;
   p->splits = splits < 1 ? 1 : (uint32_t)splits;
   p->blocks = base * p->splits;
-  return p->blocks > 0x7FFFFFFFull ? hipErrorInvalidConfiguration : hipSuccess;
+  return p->blocks > 0xFFFFFFull ? hipErrorInvalidConfiguration : hipSuccess;
 }
 
 // The workspace: [unit][split][head_dim] floats, then [unit][split] (max, sum).

@@ -503,6 +503,7 @@ hipError_t run_select(const Cache& c, const Batch& b, const void* bounds, uint32
                       const Rows& q, uint32_t n_first, uint32_t n_last, uint32_t n_select,
                       int32_t* sel, void* workspace, hipStream_t s) {
   const uint32_t items = b.n_rows * c.n_heads;
+  if (items > 0xFFFFFFFFull / (b.max_pages <= 1024 ? 256 : 1024)) return hipErrorInvalidConfiguration;
   Scores sc = {nullptr, nullptr, nullptr, padded_pages(b)};
   if (b.max_pages > n_select) {
     sc.exact = (uint64_t*)workspace;
@@ -514,7 +515,7 @@ hipError_t run_select(const Cache& c, const Batch& b, const void* bounds, uint32
     const uint32_t rows = 16u >> padded_log2;
     const uint32_t tiles = (b.max_q + rows - 1) / rows;
     const uint64_t blocks = (uint64_t)b.n_seqs * tiles * (sc.pages / kScorePages) * c.n_heads;
-    if (blocks > 0x7FFFFFFFull) return hipErrorInvalidConfiguration;
+    if (blocks > 0xFFFFFFull) return hipErrorInvalidConfiguration;
 #define IBP_KV_SCORE(DP)                                                                            \
   hipLaunchKernelGGL((k_kv_score<T, DP>), dim3((uint32_t)blocks), dim3(256), 0, s, c, b,            \
                      (const T*)bounds, n_bounds, q, n_first, n_last, n_select, tiles, padded_log2, sc)

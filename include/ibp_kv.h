@@ -76,8 +76,8 @@ typedef struct {
  *               first ceil(max_kv / page_tokens) are read where kv_len needs
  *               them; an entry outside [0, n_pages) is a page that is not
  *               there: its tokens are seen by no query.
- *   n_rows      rows of the batch (of q and out); < 2^31.  Rows that belong to
- *               no sequence are left as they were.
+ *   n_rows      rows of the batch (of q and out); rows x query heads below 2^24.
+ *               Rows that belong to no sequence are left as they were.
  *   max_q       at least every q_start[s+1] - q_start[s]; new tokens of a
  *               sequence past the first max_q are left as they were.
  *   max_kv      at least every kv_len[s]; tokens at positions >= max_kv are
@@ -112,7 +112,8 @@ typedef struct {
  *              head's channels.  eps >= 0, finite.
  * The arithmetic is in 32 bits and is rounded once, at the end.
  * Errors: NULL pointer; sizes (rope_dim not a multiple of 16 or > head_dim,
- * head counts, n_tokens >= 2^31, rows of q_out that overlap); alignment; flags.
+ * head counts, n_tokens >= 2^31, rows of q_out that overlap, k and v of the
+ * cache the same memory); alignment; flags.
  */
 #define IBP_KV_ROPE_INTERLEAVED 1u
 int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *k, const ibp_kv_rows *v,

@@ -563,3 +563,126 @@ def test_graph_replay_and_streams():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o, want[0])
+
+
+def test_graph_of_a_prompt_chunk():
+    """Chunks over the cache (many rows, keys split over workgroups) and their selection captured
+    in two graphs that share a workspace, replayed in turn with other lengths and inputs."""
+    c = K.Case([(40, 700), (70, 300)], dtype=F16, d=64, h=2, group=2, page=16, fill=math.nan)
+    k, v = c.pools()
+    cache, batch = kv.Cache(k, v), gpu_batch(c, max_kv=704)
+    q = c.wide_q.cuda()[:, :4].contiguous()
+    bounds = K.all_bounds(c).cuda()
+    w = ws(max(kv.attend_workspace(cache, batch, c.n, 4), kv.select_workspace(cache, batch, c.n, 6),
+               kv.attend_selected_workspace(cache, batch, c.n, 4, 6)))
+
+    def dense(out, lse):
+        kv.attend(cache, batch, q, out, 0.125, lse=lse, workspace=w)
+
+    def sparse(out, lse, sel):
+        kv.select(cache, batch, bounds, q, sel, n_first=1, n_last=1, workspace=w)
+        kv.attend_selected(cache, batch, q, sel, out, 0.125, lse=lse, workspace=w)
+
+    def buffers():
+        return [torch.zeros_like(q), torch.zeros((c.n, 4), device="cuda"), torch.zeros_like(q),
+                torch.zeros((c.n, 4), device="cuda"),
+                torch.zeros((c.n, 2, 6), dtype=torch.int32, device="cuda")]
+    got, want = buffers(), buffers()
+    dense(*got[:2])
+    sparse(*got[2:])
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    log("capture chunk")
+    with torch.cuda.graph(graphs[0]):
+        dense(*got[:2])
+    with torch.cuda.graph(graphs[1]):
+        sparse(*got[2:])
+    for rep in range(3):
+        q.copy_(torch.randn_like(q))
+        batch._keep[1].copy_(torch.tensor([700 - 100 * rep, 300 - 115 * rep]))
+        dense(*want[:2])
+        sparse(*want[2:])
+        torch.cuda.synchronize()
+        for t in got:
+            t.fill_(5)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), rep
+        c.q = q.cpu()
+        c.lens = [(40, 700 - 100 * rep), (70, 300 - 115 * rep)]
+        K.check_attention(c, got[0], got[1], K.attention(c, 0.125), f"chunk replay {rep}")
+
+
+@pytest.mark.parametrize("q_len", [1, 50])
+def test_pages_beyond_32_bit_offsets(q_len):
+    """A pool of more than 2^32 elements, its pages used at both ends: every call."""
+    page, h, d = 64, 8, 128
+    n_pages = (1 << 32) // (page * h * d) + 40
+    pools = [torch.empty((n_pages, page, h, d), dtype=BF16, device="cuda") for _ in "kv"]
+    c = K.Case([(q_len, 900), (q_len, 333)], dtype=BF16, d=d, h=h, group=2, page=page)
+    where = torch.arange(c.n_pages)
+    where = torch.where(where % 2 == 0, n_pages - 1 - where, where)  # page of the small pool -> here
+    log(f"far pages q={q_len}")
+    for big, small in zip(pools, (c.k, c.v)):
+        big[where.cuda()] = small.cuda()
+    far = torch.where(c.table >= 0, where[c.table.clamp(min=0).long()].int(), c.table)
+    cache = kv.Cache(*pools)
+    batch = kv.Batch(c.q_start.cuda(), c.kv_len.cuda(), far.cuda(), q_len, 900)
+    # the last new token of each sequence again, through append
+    slots = torch.tensor([int(far[s, (n - 1) // page]) * page + (n - 1) % page
+                          for s, (_, n) in enumerate(c.lens)])
+    assert int(slots.max()) * h * d > 1 << 32
+    kk, vv = (torch.stack([x[int(c.table[s, (n - 1) // page]), (n - 1) % page]
+                           for s, (_, n) in enumerate(c.lens)]) for x in (c.k, c.v))
+    for big in pools:
+        big.view(-1, h, d)[slots.cuda()] = 9.0
+    kv.append(cache, kk.cuda(), vv.cuda(), slots.cuda())
+    bounds = torch.zeros((n_pages, h, 2, d), dtype=BF16, device="cuda")
+    kv.page_bounds(cache, kv.Batch(torch.tensor([0, 900, 1233], dtype=torch.int32).cuda(),
+                                   c.kv_len.cuda(), far.cuda(), 900, 900), bounds)
+    small_bounds = K.all_bounds(c)
+    assert torch.equal(bounds[where.cuda()].cpu()[c.table[0, :15].long()],
+                       small_bounds[c.table[0, :15].long()])
+    q = c.wide_q.cuda()[:, :2 * h]
+    out = torch.zeros((c.n, 2 * h, d), dtype=BF16, device="cuda")
+    lse = torch.zeros((c.n, 2 * h), device="cuda")
+    kv.attend(cache, batch, q, out, 0.1, lse=lse,
+              workspace=ws(kv.attend_workspace(cache, batch, c.n, 2 * h)))
+    K.check_attention(c, out, lse, K.attention(c, 0.1), "far pages")
+    sel = torch.zeros((c.n, h, 4), dtype=torch.int32, device="cuda")
+    kv.select(cache, batch, bounds, q, sel, n_first=0, n_last=1,
+              workspace=ws(kv.select_workspace(cache, batch, c.n, 4)))
+    want = K.select(c, small_bounds, 0, 1, 4)
+    assert torch.equal(sel.cpu(), want)
+    kv.attend_selected(cache, batch, q, sel, out, 0.1, lse=lse,
+                       workspace=ws(kv.attend_selected_workspace(cache, batch, c.n, 2 * h, 4)))
+    K.check_attention(c, out, lse, K.attention(c, 0.1, sel=want), "far pages, selected")
+
+
+def test_empty_calls():
+    """No tokens, no rows, no sequences, a cache whose sequences are all empty."""
+    c = K.Case([(0, 0), (0, 40)], d=64, tail_rows=3)
+    k, v = c.pools()
+    cache = kv.Cache(k, v)
+    empty = torch.zeros((0, 2, 64), dtype=BF16, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    none = kv.Batch(i32(0), i32(), torch.zeros((0, 4), dtype=torch.int32, device="cuda"), 0, 0)
+    log("empty calls")
+    kv.append(cache, empty, empty, torch.zeros(0, dtype=torch.int64, device="cuda"))
+    bounds = torch.full((c.n_pages, 2, 2, 64), PAD, dtype=BF16, device="cuda")
+    q = torch.zeros((3, 4, 64), dtype=BF16, device="cuda")
+    out = torch.full_like(q, PAD)
+    sel = torch.full((3, 2, 5), -7, dtype=torch.int32, device="cuda")
+    for batch in (none, gpu_batch(c), kv.Batch(c.q_start.cuda(), c.kv_len.cuda(), c.table.cuda(), 2, 48)):
+        for n in (0, 3):
+            kv.page_bounds(cache, batch, bounds)
+            kv.attend(cache, batch, q[:n], out[:n], 1.0,
+                      workspace=ws(kv.attend_workspace(cache, batch, n, 4)))
+            kv.select(cache, batch, bounds, q[:n], sel[:n], n_first=0, n_last=1,
+                      workspace=ws(kv.select_workspace(cache, batch, n, 5)))
+            kv.attend_selected(cache, batch, q[:n], sel[:n], out[:n], 1.0,
+                               workspace=ws(kv.attend_selected_workspace(cache, batch, n, 4, 5)))
+    torch.cuda.synchronize()
+    assert (out == PAD).all() and (sel == -7).all() and (bounds == PAD).all()

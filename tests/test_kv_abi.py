@@ -47,7 +47,7 @@ def refused(code, fn, *a, **kw):
 
 
 def cache(kv, **kw):
-    a = dict(k=P, v=P, n_pages=10, page_tokens=16, n_heads=2, head_dim=64, dtype=kv.BF16)
+    a = dict(k=P, v=3 * P, n_pages=10, page_tokens=16, n_heads=2, head_dim=64, dtype=kv.BF16)
     a.update(kw)
     return kv.Cache.from_pointers(**a)
 
@@ -112,7 +112,7 @@ def test_append_refusals(kv):
         call(ibp.ERR_SIZE, k_norm=P, eps=eps)
     call(ibp.ERR_FLAGS, flags=2)
     call(ibp.ERR_SIZE, n_tokens=1 << 31)
-    call(ibp.ERR_SIZE, n_tokens=(1 << 31) // 4, k=kv.Rows(P, 0, 64, 2), v=kv.Rows(P, 0, 64, 2))
+    refused(ibp.ERR_SIZE, kv.append, cache(kv, v=P), good, good, P, n_tokens=3, stream=0)  # one pool
     with pytest.raises(ValueError):
         kv.append(c, good, good, P, stream=0)
 
@@ -142,7 +142,11 @@ def test_batch_and_attend_refusals(kv):
     call(ibp.ERR_ALIGN, out=kv.Rows(2 * P + 8, 256, 64, 4))
     call(ibp.ERR_ALIGN, lse=P + 2)
     call(ibp.ERR_SIZE, n_rows=1 << 31)
-    call(ibp.ERR_SIZE, n_rows=1 << 29)                              # x 4 heads
+    call(ibp.ERR_SIZE, n_rows=1 << 22)                              # x 4 heads
+    # more workgroups than a launch takes: the largest batch of the longest sequences
+    big = batch(kv, n_seqs=1 << 25, table_stride=8)
+    if torch.cuda.device_count() > 0:
+        call(ibp.ERR_SIZE, b=big)
     for s in (float("nan"), float("inf")):
         call(ibp.ERR_SIZE, scale=s)
     call(ibp.ERR_FLAGS, flags=2)
