@@ -13,10 +13,12 @@ namespace {
 //   heads  Four key heads to a workgroup where their number allows: its waves then read
 //          neighbouring parts of the same token rows (OPT-13B decode 172 -> 162 us), instead of
 //          different keys of one head.
-//   splits The keys of a row tile over several workgroups until the GPU has eight (few) or two
-//          a CU: more than it runs at a time, so that the last ones to finish are short (few: 4
-//          a CU 175 / 340 us, 8 172 / 314, 12 166 / 320 for OPT-13B decode / 131072-token
-//          contexts), but no split below 256 keys of a wave's turn (few) or 512.
+//   splits The keys of a row tile over several workgroups until the GPU has eight a CU (few:
+//          more than it runs at a time, so that the last ones to finish are short; 4 a CU took
+//          175 / 340 us, 8 172 / 314, 12 166 / 320 for OPT-13B decode / 131072-token contexts)
+//          or two (many rows: as many as it runs; more only add partial results to write and
+//          join, 2048 tokens of 32 heads 62 us with two, 74 with four), but no split below 256
+//          keys of a wave's turn (few) or 512.
 // A window bounds the keys of a tile; the workspace is sized without one, for as many splits or
 // more.
 hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,

@@ -346,7 +346,54 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
   }
 }
 
-// The splits of a row together: a workgroup per (row, head).  Each split's factor first, from
+// The splits of a row together, few of them (of chunks, many rows): 16, 32 or 64 lanes a (row,
+// head), four channels each; every lane forms the factors by itself.
+constexpr uint32_t kFewSplits = 8;
+
+template <typename T>
+__global__ __launch_bounds__(256) void k_kv_join_few(Batch b, Rows out, Partial part, uint32_t lanes,
+                                                     float* __restrict__ lse) {
+  const uint32_t per = 256 / lanes;
+  const uint64_t units = (uint64_t)b.n_rows * out.n_heads;
+  const uint64_t unit = (uint64_t)blockIdx.x * per + threadIdx.x / lanes;
+  if (unit >= units) return;
+  const uint32_t row = (uint32_t)(unit / out.n_heads), head = (uint32_t)(unit % out.n_heads);
+  if (seq_of_row(b, (int32_t)row) < 0) return;
+  const uint32_t c = threadIdx.x % lanes * 4;
+  const bool live = c < part.head_dim;
+  float2 x[kFewSplits];
+  f32x4 y[kFewSplits];
+  float mm = -INFINITY;
+#pragma unroll
+  for (uint32_t e = 0; e < kFewSplits; ++e) {
+    if (e >= part.splits) break;
+    x[e] = part.ms[unit * part.splits + e];
+    y[e] = live ? *(const f32x4*)(part.row(unit, e) + c) : f32x4{0.f, 0.f, 0.f, 0.f};
+    mm = fmaxf(mm, x[e].x);
+  }
+  const float base = mm == -INFINITY ? 0.f : mm;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  float z = 0.f;
+#pragma unroll
+  for (uint32_t e = 0; e < kFewSplits; ++e) {
+    if (e >= part.splits) break;
+    const float f = exp2_raw(x[e].x - base);
+    z += f * x[e].y;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] += f == 0.f ? 0.f : f * y[e][r];
+  }
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  if (live) {
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    t4 v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = (T)(o[r] * inv);
+    *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
+  }
+  if (lse && c == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
+}
+
+// The splits of a row together, many of them: a workgroup per (row, head).  Each split's factor first, from
 // the maxima; then 16, 32 or 64 lanes (four channels each) a split, as many splits at
 // a time as the workgroup holds.
 template <typename T>
@@ -454,11 +501,19 @@ hipError_t launch_join(uint32_t dtype, const Batch& b, const Rows& out, Partial 
                        hipStream_t s) {
   const uint64_t units = (uint64_t)b.n_rows * out.n_heads;
   const uint32_t lanes = part.head_dim <= 64 ? 16 : part.head_dim <= 128 ? 32 : 64;
-  const dim3 grid((uint32_t)units);
-  if (dtype == IBP_KV_F16)
-    hipLaunchKernelGGL(k_kv_join<_Float16>, grid, dim3(256), 0, s, b, out, part, lanes, lse);
-  else
-    hipLaunchKernelGGL(k_kv_join<__bf16>, grid, dim3(256), 0, s, b, out, part, lanes, lse);
+  const bool few = part.splits <= kFewSplits;
+  const uint32_t per = few ? 256 / lanes : 1;
+  const dim3 grid((uint32_t)((units + per - 1) / per));
+#define IBP_KV_JOIN(KERNEL, T) \
+  hipLaunchKernelGGL(KERNEL<T>, grid, dim3(256), 0, s, b, out, part, lanes, lse)
+  if (dtype == IBP_KV_F16) {
+    if (few) IBP_KV_JOIN(k_kv_join_few, _Float16);
+    else IBP_KV_JOIN(k_kv_join, _Float16);
+  } else {
+    if (few) IBP_KV_JOIN(k_kv_join_few, __bf16);
+    else IBP_KV_JOIN(k_kv_join, __bf16);
+  }
+#undef IBP_KV_JOIN
   return hipGetLastError();
 }
 
