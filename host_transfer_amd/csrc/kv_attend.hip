@@ -42,7 +42,11 @@ hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_
   if (splits > kMaxSplits) splits = kMaxSplits;
   p->splits = splits < 1 ? 1 : (uint32_t)splits;
   p->blocks = base * p->splits;
-  return p->blocks > 0xFFFFFFull ? hipErrorInvalidConfiguration : hipSuccess;
+  // a launch's threads are counted in 32 bits: 256 a workgroup, up to 1024 a row where many
+  // splits are joined
+  const uint64_t units = (uint64_t)b.n_rows * n_q_heads;
+  return p->blocks > 0xFFFFFFull || (p->splits > 64 && units > 0x3FFFFFull)
+             ? hipErrorInvalidConfiguration : hipSuccess;
 }
 
 // The workspace: [unit][split][head_dim] floats, then [unit][split] (max, sum).

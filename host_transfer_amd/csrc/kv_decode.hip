@@ -396,22 +396,23 @@ __global__ __launch_bounds__(256) void k_kv_join_few(Batch b, Rows out, Partial 
 // The splits of a row together, many of them: a workgroup per (row, head).  Each split's factor first, from
 // the maxima; then 16, 32 or 64 lanes (four channels each) a split, as many splits at
 // a time as the workgroup holds.
-template <typename T>
-__global__ __launch_bounds__(256) void k_kv_join(Batch b, Rows out, Partial part, uint32_t lanes,
+template <typename T, uint32_t kJoinThreads>
+__global__ __launch_bounds__(kJoinThreads) void k_kv_join(Batch b, Rows out, Partial part, uint32_t lanes,
                                                  float* __restrict__ lse) {
   __shared__ float s_f[kMaxSplits];
-  __shared__ float s_red[kWaves];
-  __shared__ f32x4 s_o[256];
+  constexpr uint32_t NW = kJoinThreads / kWave;
+  __shared__ float s_red[NW];
+  __shared__ f32x4 s_o[kJoinThreads];
   const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const uint64_t unit = blockIdx.x;
   const uint32_t row = (uint32_t)(unit / out.n_heads), head = (uint32_t)(unit % out.n_heads);
   if (seq_of_row(b, (int32_t)row) < 0) return;
   const float2* ms = part.ms + unit * part.splits;
-  float2 x[kMaxSplits / 256];
+  float2 x[kMaxSplits / kJoinThreads];
   float mm = -INFINITY;
 #pragma unroll
-  for (uint32_t a = 0; a < kMaxSplits / 256; ++a) {
-    const uint32_t e = tid + a * 256;
+  for (uint32_t a = 0; a < kMaxSplits / kJoinThreads; ++a) {
+    const uint32_t e = tid + a * kJoinThreads;
     x[a] = e < part.splits ? ms[e] : make_float2(-INFINITY, 0.f);
     mm = fmaxf(mm, x[a].x);
   }
@@ -419,13 +420,13 @@ __global__ __launch_bounds__(256) void k_kv_join(Batch b, Rows out, Partial part
   for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d, kWave));
   if (lane == 0) s_red[wave] = mm;
   __syncthreads();
-  mm = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  for (uint32_t w = 0; w < NW; ++w) mm = fmaxf(mm, s_red[w]);
   __syncthreads();
   const float base = mm == -INFINITY ? 0.f : mm;
   float z = 0.f;
 #pragma unroll
-  for (uint32_t a = 0; a < kMaxSplits / 256; ++a) {
-    const uint32_t e = tid + a * 256;
+  for (uint32_t a = 0; a < kMaxSplits / kJoinThreads; ++a) {
+    const uint32_t e = tid + a * kJoinThreads;
     const float f = exp2_raw(x[a].x - base);
     if (e < part.splits) {
       s_f[e] = f;
@@ -436,9 +437,10 @@ __global__ __launch_bounds__(256) void k_kv_join(Batch b, Rows out, Partial part
   for (int d = 1; d < kWave; d <<= 1) z += __shfl_xor(z, d, kWave);
   if (lane == 0) s_red[wave] = z;
   __syncthreads();
-  z = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+  z = 0.f;
+  for (uint32_t w = 0; w < NW; ++w) z += s_red[w];
   const uint32_t c = (tid % lanes) * 4;
-  const uint32_t at_once = 256 / lanes;
+  const uint32_t at_once = kJoinThreads / lanes;
   f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
   if (c < part.head_dim) {
 #pragma unroll 4
@@ -451,12 +453,16 @@ __global__ __launch_bounds__(256) void k_kv_join(Batch b, Rows out, Partial part
   }
   s_o[tid] = o;
   __syncthreads();
-  if (tid < lanes && c < part.head_dim) {
-    for (uint32_t a = 1; a < at_once; ++a) {
-      const f32x4 y = s_o[a * lanes + tid];
+  for (uint32_t half = kJoinThreads / 2; half >= lanes; half /= 2) {
+    if (tid < half) {
+      const f32x4 y = s_o[tid + half];
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[r] += y[r];
+      s_o[tid] = o;
     }
+    __syncthreads();
+  }
+  if (tid < lanes && c < part.head_dim) {
     const float inv = z == 0.f ? 0.f : 1.f / z;
     typedef T t4 __attribute__((ext_vector_type(4)));
     t4 v;
@@ -501,17 +507,23 @@ hipError_t launch_join(uint32_t dtype, const Batch& b, const Rows& out, Partial 
                        hipStream_t s) {
   const uint64_t units = (uint64_t)b.n_rows * out.n_heads;
   const uint32_t lanes = part.head_dim <= 64 ? 16 : part.head_dim <= 128 ? 32 : 64;
+  // (11 splits of 800 rows and heads 5.8 us with 256 threads each, 10.6 with 1024; 256 splits of
+  // 128 20 us with 256, 10 with 1024)
+  const uint32_t threads = part.splits > 64 ? 1024 : 256;
   const bool few = part.splits <= kFewSplits;
   const uint32_t per = few ? 256 / lanes : 1;
   const dim3 grid((uint32_t)((units + per - 1) / per));
-#define IBP_KV_JOIN(KERNEL, T) \
-  hipLaunchKernelGGL(KERNEL<T>, grid, dim3(256), 0, s, b, out, part, lanes, lse)
+#define IBP_KV_JOIN(T)                                                                           \
+  if (few)                                                                                       \
+    hipLaunchKernelGGL(k_kv_join_few<T>, grid, dim3(256), 0, s, b, out, part, lanes, lse);       \
+  else if (threads == 256)                                                                       \
+    hipLaunchKernelGGL((k_kv_join<T, 256>), grid, dim3(256), 0, s, b, out, part, lanes, lse);    \
+  else                                                                                           \
+    hipLaunchKernelGGL((k_kv_join<T, 1024>), grid, dim3(1024), 0, s, b, out, part, lanes, lse);
   if (dtype == IBP_KV_F16) {
-    if (few) IBP_KV_JOIN(k_kv_join_few, _Float16);
-    else IBP_KV_JOIN(k_kv_join, _Float16);
+    IBP_KV_JOIN(_Float16)
   } else {
-    if (few) IBP_KV_JOIN(k_kv_join_few, __bf16);
-    else IBP_KV_JOIN(k_kv_join, __bf16);
+    IBP_KV_JOIN(__bf16)
   }
 #undef IBP_KV_JOIN
   return hipGetLastError();

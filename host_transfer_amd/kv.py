@@ -225,10 +225,15 @@ def _rows(name, cache, t, n_tokens, dev):
     n = shape[0]
     if n_tokens is not None and n != n_tokens:
         raise ValueError(f"{name}: {n_tokens} tokens needed, got {n}")
-    s = _strides(t)
-    if s[2] != 1:
+    s0, s1, s2 = t.stride()
+    heads, head_dim = shape[1], shape[2]
+    if s2 != 1 and head_dim > 1:
         raise ValueError(f"{name}: channels must be contiguous")
-    return _CRows(t.data_ptr(), s[0], s[1], shape[1]), n
+    if heads == 1:  # the stride of an axis of size 1 addresses nothing
+        s1 = head_dim
+    if n == 1:
+        s0 = heads * s1
+    return _CRows(t.data_ptr(), s0, s1, heads), n
 
 
 def _of_dtype(name, cache, t, numel, dev):
