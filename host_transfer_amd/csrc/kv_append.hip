@@ -29,7 +29,9 @@ __device__ __forceinline__ void store8(T* p, const float x[8]) {
 // rope_dim / 16), two neighbouring ones elsewhere.  So the token's cosines and
 // sines, its slot and the norms' weights are read once and stay in registers for all of its
 // heads; what is left is one pass over the rows.  The norm's sum of squares goes over the L
-// lanes by butterflies.  Bound by reading and writing the rows.
+// lanes by butterflies.  Bound by reading and writing the rows: 16,000 tokens of 32 + 8 + 8
+// heads of 128 (402 MB) 79 us, 5.1 TB/s; with a group of lanes per (token, head), each reading
+// its part of the rotation, 292 us.
 template <typename T, int L>
 __global__ __launch_bounds__(256) void k_kv_append(Cache cache, Rows k, Rows v, Rows q, Rows q_out,
                                                    const int64_t* __restrict__ slots,
@@ -178,7 +180,9 @@ __device__ __forceinline__ T nan_max(T a, T b) {
   return (b > a || b != b) ? b : a;
 }
 
-// A thread per (page, head, eight channels): it walks the page's tokens.
+// A thread per (page, head, eight channels): it walks the page's tokens, eight loads in flight
+// (one at a time 34 us where this takes 27).  Bound by reading the keys: 1,639 pages of 32 tokens,
+// 8 heads of 128 (114 MB) 27 us, 4.2 TB/s; two or four threads a piece 25 to 27 us.
 template <typename T>
 __global__ __launch_bounds__(256) void k_kv_page_bounds(Cache cache, Batch b, T* __restrict__ bounds,
                                                         uint32_t pages_per_seq, uint32_t chunks) {

@@ -28,6 +28,10 @@ constexpr int kWaves = 4;
 // the transposed read gives the second product's operand.  LDS rows are padded by
 // 32 B: the eight rows that half a wave reads then lie in eight different 32 B
 // windows of the banks for every head_dim that is a multiple of 32.
+//
+// Measured (with the join): 20 sequences of up to 2,048 tokens, 40 heads (814 MB) 162 us, 5.0 TB/s;
+// 4 sequences of up to 131,072 tokens, 32 query heads on 8 key heads (1.61 GB) 300 us, 5.4 TB/s, as
+// a large copy runs; 8 rows' lists of 2,048 tokens (67 MB) 23 us.
 template <typename T, int DP, bool kSelected, int kHeads>
 __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q, Rows out,
                                                    const int32_t* __restrict__ sel,
