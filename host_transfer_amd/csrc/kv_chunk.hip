@@ -31,9 +31,11 @@ __device__ __forceinline__ void load_lds(const void* p, uint32_t lds) {
                :: "s"(lds), "v"(p) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds(const void* base, uint32_t offset, uint32_t lds) {
-  // (five wait states, should the base come straight from a lane: the compiler does not look in here)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(lds), "v"(offset), "s"(base) : "memory", "m0");
+  // The move fills the wait state after m0; and a base that came straight from a lane would need
+  // five before the load, which the compiler does not see to in here, but none before a move.
+  uint64_t scalar;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+               : "=&s"(scalar) : "s"(lds), "v"(offset), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
