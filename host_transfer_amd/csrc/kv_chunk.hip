@@ -60,7 +60,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 //
 // Measured (bf16, 32 query heads on 8 key heads, head_dim 128): one prompt of 16,384 tokens
 // 2.09 ms, 1.05 PFLOP/s, where a library product of 16,384^3 reaches 1.31 on the same card; the
-// matrix cores are busy 52 % of the time, the vector ALU 57 %, at the 1.9 GHz that power
+// matrix cores are busy 52 % of the time, the vector ALU 56 %, at the 1.9 GHz that power
 // leaves.  Without the pipeline (rows through registers, scores, weights and values in turn) it
 // took 2.49 ms.  No faster: 64 rows a wave, one wave a SIMD (2.09 ms; ragged chunks 380 against 290
 // us), half of the weights beside the values instead of the scores (the same).
