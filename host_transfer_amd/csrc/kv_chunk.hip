@@ -248,9 +248,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     }
   };
   // Scores of step t0 that the row does not see to -inf, where there may be any (`most`, the
-  // largest one, is then found anew); then the base that the exponents are taken against: it
-  // follows the maximum only when that passes it by 2^8: weights then stay below 2^8 (as exact
-  // in the dtype as below 1, and far from its largest number), and most steps need no rescaling.
+  // largest one, is then found anew); then the base that the exponents are taken against: a
+  // weight is 2^(score * mul + off).  Where a base is so large that its own rounding could lift
+  // a weight past fp16's range, the scores are first made differences, each product
+  // rounded as the base was.
+  float mul = sc2, off = 0.f;
   auto bound = [&](int32_t t0, uint64_t seen, f32x16 (&sc)[2], float most) {
     if (!(seen == ~0ull && t0 >= full_lo && t0 + kKeys <= full_hi)) {
       uint32_t vis[2];
@@ -265,8 +267,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
         }
     }
     most = max_half(most) * sc2;
-    if (__any(most > top + 8.f)) {
-      const float next = fmaxf(top, most);
+    if (__any(most > top + Base<T>::kRoom)) {
+      const float next = next_base<T>(top, most);
       const float keep = exp2_raw(top - (next == -INFINITY ? 0.f : next));
       settle(o);
       z *= keep;
@@ -275,6 +277,17 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[t][r] *= keep;
       top = next;
+    }
+    mul = sc2;
+    off = top == -INFINITY ? 0.f : -top;
+    if (__any(fabsf(off) >= 0x1p20f)) {
+#pragma clang fp contract(off)
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sc[a][r] = sc[a][r] * sc2 + off;
+      mul = 1.f;
+      off = 0.f;
     }
   };
 
@@ -322,7 +335,6 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       auto k_piece = [&](int i) {
         return *(const V8<T>*)(sk + (i % 2) * 32 * DL + (((uint32_t)(i / 2 * 2) ^ k_sw) << 3));
       };
-      const float base = top == -INFINITY ? 0.f : top;
       V8<T> p[4], kf[3];
       float z0 = 0.f, z1 = 0.f;
 #pragma unroll
@@ -338,7 +350,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
         nxt[i % 2] = mfma32(kf[i % 3], qf[i / 2], nxt[i % 2]);
 #pragma unroll
         for (int e = i * 16 / KS; e < (i + 1) * 16 / KS; ++e) {
-          const float y = exp2_raw(fmaf(cur[e / 16][e % 16], sc2, -base));
+          const float y = exp2_raw(fmaf(cur[e / 16][e % 16], mul, off));
           if (e % 2) z1 += y;
           else z0 += y;
           // half a step of the dtype, relative, as the output's own rounding

@@ -233,8 +233,8 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
     float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
                        fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
     most = max_half(max_quarter(most));
-    if (__any(most > top)) {
-      const float next = fmaxf(top, most);
+    if (__any(most > top + Base<T>::kRoom)) {
+      const float next = next_base<T>(top, most);
       const float keep = exp2_raw(top - (next == -INFINITY ? 0.f : next));
       z *= keep;
 #pragma unroll
@@ -247,9 +247,10 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
     V8<T> p;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
+#pragma clang fp contract(off)  // (the product rounded as the base was: huge scores stay at most kRoom above)
       const float y = exp2_raw(x[e] - base);
       z += y;
-      p[e] = (T)y;  // <= 1: half a step of the dtype, relative, as the output's own rounding
+      p[e] = (T)y;  // half a step of the dtype, relative, as the output's own rounding
     }
     wave_sync();
 #pragma unroll

@@ -97,6 +97,30 @@ __device__ __forceinline__ float sum_quarter(float x) {
 
 __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The base that a row's exponents are taken against follows the row's largest score so far at a
+// distance: it is raised, to kLift below that score, when the score passes it by kRoom, so that
+// few steps rescale what was summed before them.  The largest weight lies between 2^kLift
+// and 2^kRoom, where its rounding is as exact as near 1.  bf16 has the range of fp32.  fp16 has none below
+// 2^-24 and its full precision only from 2^-14 up: with its weights near the type's upper end
+// 2^-26 of the largest one still has all of it, and what is lost of n smaller ones is below n * 2^-37
+// of the largest (with weights up to 1 it was n * 2^-25: 30,000 weights of 2^-25, 7.5e-4 of
+// the sum together, came out 2 % short).  Scores past 2^20 are the base themselves: their
+// distance to another base would be rounded by more than the room can bear.
+template <typename T>
+struct Base;
+template <>
+struct Base<_Float16> {
+  static constexpr float kLift = 12.f, kRoom = 15.f;
+};
+template <>
+struct Base<__bf16> {
+  static constexpr float kLift = 0.f, kRoom = 8.f;
+};
+template <typename T>
+__device__ __forceinline__ float next_base(float base, float most) {
+  return fmaxf(base, fabsf(most) < 0x1p20f ? most - Base<T>::kLift : most);
+}
+
 // 16 B from global memory through a global-address-space pointer.
 template <typename T>
 __device__ __forceinline__ V8<T> load_row8(const T* p) {
@@ -145,7 +169,7 @@ __device__ __forceinline__ bool any_odd(V8<T> v) {
 }
 
 // Where a row's partial results of the splits of its keys lie in the
-// workspace: float[unit][split][head_dim], then float2[unit][split] of (max,
+// workspace: float[unit][split][head_dim], then float2[unit][split] of (base,
 // sum); unit = row * heads + head.  Scores in the exponent of 2.
 struct Partial {
   float* o;

@@ -276,6 +276,56 @@ def test_attend_large_scores():
     K.check_attention(c, out, lse, K.attention(c, 0.25), "rising")
 
 
+@pytest.mark.parametrize("q_len", [1, 2, 40])
+def test_attend_many_small_weights(q_len):
+    """One large score and so many small ones that their sum counts, each below half of fp16's
+    smallest step next to it: weights of e^-17.5 = 2^-25.2, 30,000 of them are 7.5e-4 of the sum."""
+    n = 30000
+    c = K.Case([(q_len, n)], dtype=F16, d=16, h=1, group=1, page=64)
+    c.q[:] = 0.0
+    c.q[:, 0, 0] = 1.0
+    c.k[:], c.v[:] = 0.0, 1.0
+    c.k[:, :, 0, 0] = -17.5
+    for j in (0, n // 2):  # the large score first, or after many small ones
+        first = c.k.clone()
+        c.k[int(c.table[0, j // 64]), j % 64] = 0.0
+        c.v[int(c.table[0, j // 64]), j % 64] = 0.0
+        log(f"many small weights, {q_len} rows, large score at {j}")
+        out, lse = run_attend(c, 1.0, causal=False)
+        want = (n - 1) * math.exp(-17.5) / (1 + (n - 1) * math.exp(-17.5))
+        # a weight off by half a step of fp16 and, of the exponent's 18 * log2(e), 2^-24 of it
+        # eight times; the sums of equal terms by less than n of these; the output once
+        tol = want * (2 ** -11 + 2 ** -11 + 8 * 26 * 2.0 ** -24 + n * 2.0 ** -24)
+        assert (out.double() - want).abs().max() <= tol, (float(out.max()), want)
+        c.k, c.v[:] = first, 1.0
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_attend_fp16_huge_scores(q_len):
+    """Scores up to 2^35: differences of scores are then far above 1 or exactly 0, so the row's
+    result is the mean of the values of its largest score's keys."""
+    for top in (600.0, 4000.0, 60000.0):
+        c = K.Case([(q_len, 700)], dtype=F16, d=128, h=1, group=2, page=16)
+        c.q[:] = 1.0
+        c.q[:, 1] = top
+        best = [5, 300, 301, 698]  # by an eighth above all others
+        at = lambda j: (int(c.table[0, j // 16]), j % 16)
+        c.k[:] = top * 7 / 8
+        for j in best:
+            c.k[at(j)] = top
+        log(f"huge scores {top}, {q_len} rows")
+        out, lse = run_attend(c, 0.7, causal=False)
+        v = torch.stack([c.v[at(j)] for j in best]).double()[:, 0]
+        # four equal weights y, of any size between two powers of two: the sum takes 4 y, the values
+        # are multiplied by y rounded to fp16, y (1 + d) with |d| <= 2^-11, so the quotient
+        # is the mean times 1 + d; it is rounded again, by 2^-11; sums of four and the quotient in fp32
+        tol = 2 * 2 ** -11 * v.mean(0).abs() + 16 * 2.0 ** -24 * v.abs().mean(0) + 2.0 ** -25
+        for h in range(2):
+            assert ((out[:, h].cpu().double() - v.mean(0)).abs() <= tol).all(), (top, h)
+            want = 0.7 * 128 * float(c.k.max()) * (1.0, top)[h] + math.log(4)
+            assert ((lse[:, h].cpu().double() - want).abs() <= (128 + 16) * 2.0 ** -24 * want).all()
+
+
 # ---------------------------------------------------------------- selection
 
 SEL_LENS = [(1, 1), (1, 500), (0, 0), (7, 333), (1, 16), (3, 17), (1, 999), (2, 1), (40, 260)]
