@@ -204,7 +204,8 @@ int attend(const char* name, const ibp_kv_cache* cache, const ibp_kv_batch* batc
     return set_error(IBP_ERR_SIZE, "%s: out has %u heads, q has %u", name, orow.n_heads, qr.n_heads);
   if (b.n_rows && orow.p == qr.p)
     return set_error(IBP_ERR_SIZE, "%s: out must not overlap q", name);
-  if (!isfinite(scale)) return set_error(IBP_ERR_SIZE, "%s: scale must be finite", name);
+  if (!(fabsf(scale) <= 0x1p126f))  // (scores are in the exponent of 2: times 1.44)
+    return set_error(IBP_ERR_SIZE, "%s: scale must be finite, its magnitude at most 2^126", name);
   if (n_select && b.n_rows) {
     if (!sel) return set_error(IBP_ERR_NULL, "%s: sel is required", name);
     if (!aligned(sel, 4)) return set_error(IBP_ERR_ALIGN, "%s: misaligned sel", name);

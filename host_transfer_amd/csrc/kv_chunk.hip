@@ -132,8 +132,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
 #pragma unroll
   for (int k = 0; k < KS; ++k) {
     const uint32_t c = k * 16 + half * 8;
-    qf[k] = load_row8(have && c < hd && scale != 0.f ? qp + c : zeros);
+    qf[k] = load_row8(have && c < hd ? qp + c : zeros);
     if (scale < 0.f) qf[k] = -qf[k];
+    if (scale == 0.f)  // (zeros, but for what is no number)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) qf[k][e] = isfinite((float)qf[k][e]) ? (T)0.f : (T)NAN;
   }
   const float sc2 = scale == 0.f ? 1.f : fabsf(scale) * kLog2e;
 

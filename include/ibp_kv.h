@@ -153,7 +153,7 @@ int ibp_kv_page_bounds(const ibp_kv_cache *cache, const ibp_kv_batch *batch, voi
  * Scores, the softmax and the sums are in 32 bits; the weights exp(s - max)
  * are rounded to the cache's dtype where they multiply V.
  * Errors: NULL pointer; sizes (workspace too small; a grid past the
- * hardware's limits); alignment; unknown flags; scale not finite.
+ * hardware's limits); alignment; unknown flags; scale not finite or past 2^126.
  */
 #define IBP_KV_CAUSAL 1u
 int ibp_kv_attend(const ibp_kv_cache *cache, const ibp_kv_batch *batch, const ibp_kv_rows *q,

@@ -326,6 +326,17 @@ def test_attend_fp16_huge_scores(q_len):
             assert ((lse[:, h].cpu().double() - want).abs() <= (128 + 16) * 2.0 ** -24 * want).all()
 
 
+def test_attend_scale_zero():
+    """All seen keys weigh the same; a query or key that is no number still makes its rows NaN."""
+    for q_len in (1, 40):
+        c = K.Case([(q_len, 90), (q_len, 70)], dtype=BF16, d=64, h=1, group=2, page=16)
+        c.q[0, 1, 3] = math.nan
+        c.q[q_len, 0, 60] = math.inf
+        log(f"scale 0, {q_len} rows")
+        out, lse = run_attend(c, 0.0)
+        K.check_attention(c, out, lse, K.attention(c, 0.0), f"scale 0, {q_len} rows")
+
+
 # ---------------------------------------------------------------- selection
 
 SEL_LENS = [(1, 1), (1, 500), (0, 0), (7, 333), (1, 16), (3, 17), (1, 999), (2, 1), (40, 260)]

@@ -157,6 +157,15 @@ def test_batch_and_attend_refusals(kv):
         kv.attend(c, batch(kv), q, o, 1.0, stream=0)
 
 
+def test_scale_past_the_exponents(kv):
+    from host_transfer_amd import ibp
+    q, o = kv.Rows(P, 256, 64, 4), kv.Rows(2 * P, 256, 64, 4)
+    for s in (2.0 ** 127, -3e38):
+        refused(ibp.ERR_SIZE, kv.attend, cache(kv), batch(kv), q, o, s, n_rows=3, stream=0)
+        refused(ibp.ERR_SIZE, kv.attend_selected, cache(kv), batch(kv), q, P, o, s, n_select=4, n_rows=3,
+                stream=0)
+
+
 def test_select_refusals(kv):
     from host_transfer_amd import ibp
     c = cache(kv)
