@@ -122,9 +122,10 @@ int check_rows(const char* name, const char* what, const ibp_kv_rows* r, uint64_
   return IBP_OK;
 }
 
-// pointers: the arrays are read (a workspace query passes false).
+// pointers: the arrays are read (a workspace query passes false).  rows: the call has rows, and
+// no sequence more than all of them: a larger max_q is none of the launch's size.
 int check_batch(const char* name, const ibp_kv_batch* b, const ibp::kv::Cache& c, bool pointers,
-                ibp::kv::Batch* out) {
+                bool rows, ibp::kv::Batch* out) {
   if (!b) return set_error(IBP_ERR_NULL, "%s: batch is required", name);
   if (b->n_rows > 0x7FFFFFFFull || b->n_seqs > 0x7FFFFFFFu || b->max_q > 0x7FFFFFFFu)
     return set_error(IBP_ERR_SIZE, "%s: n_rows, n_seqs and max_q must be below 2^31", name);
@@ -149,7 +150,7 @@ int check_batch(const char* name, const ibp_kv_batch* b, const ibp::kv::Cache& c
   out->table_stride = b->table_stride;
   out->n_rows = (uint32_t)b->n_rows;
   out->n_seqs = b->n_seqs;
-  out->max_q = b->max_q;
+  out->max_q = rows && b->max_q > b->n_rows ? (uint32_t)b->n_rows : b->max_q;
   out->max_kv = b->max_kv;
   out->max_pages = max_pages;
   return IBP_OK;
@@ -195,7 +196,7 @@ int attend(const char* name, const ibp_kv_cache* cache, const ibp_kv_batch* batc
   ibp::kv::Batch b;
   ibp::kv::Rows qr, orow;
   int r;
-  if ((r = check_cache(name, cache, true, &c)) || (r = check_batch(name, batch, c, true, &b)) ||
+  if ((r = check_cache(name, cache, true, &c)) || (r = check_batch(name, batch, c, true, true, &b)) ||
       (r = check_rows(name, "q", q, b.n_rows, c.head_dim, false, &qr)) ||
       (r = check_rows(name, "out", out, b.n_rows, c.head_dim, true, &orow)) ||
       (r = check_group(name, c, qr.n_heads)) || (r = check_items(name, b.n_rows, qr.n_heads)))
@@ -230,7 +231,7 @@ int attend_workspace(const char* name, const ibp_kv_cache* cache, const ibp_kv_b
   ibp::kv::Cache c;
   ibp::kv::Batch b;
   int r;
-  if ((r = check_cache(name, cache, false, &c)) || (r = check_batch(name, batch, c, false, &b)) ||
+  if ((r = check_cache(name, cache, false, &c)) || (r = check_batch(name, batch, c, false, true, &b)) ||
       (r = check_group(name, c, n_q_heads)) || (r = check_items(name, b.n_rows, n_q_heads)) ||
       (r = require_device(name)))
     return r;
@@ -305,7 +306,8 @@ int ibp_kv_page_bounds(const ibp_kv_cache* cache, const ibp_kv_batch* batch, voi
   ibp::kv::Cache c;
   ibp::kv::Batch b;
   int r;
-  if ((r = check_cache(name, cache, true, &c)) || (r = check_batch(name, batch, c, true, &b)))
+  if ((r = check_cache(name, cache, true, &c)) ||
+      (r = check_batch(name, batch, c, true, false, &b)))
     return r;
   if (!bounds) return set_error(IBP_ERR_NULL, "%s: bounds is required", name);
   if (!aligned(bounds, 16)) return set_error(IBP_ERR_ALIGN, "%s: misaligned bounds", name);
@@ -341,7 +343,7 @@ int ibp_kv_select(const ibp_kv_cache* cache, const ibp_kv_batch* batch, const vo
   ibp::kv::Batch b;
   ibp::kv::Rows qr;
   int r;
-  if ((r = check_cache(name, cache, false, &c)) || (r = check_batch(name, batch, c, true, &b)) ||
+  if ((r = check_cache(name, cache, false, &c)) || (r = check_batch(name, batch, c, true, true, &b)) ||
       (r = check_rows(name, "q", q, b.n_rows, c.head_dim, false, &qr)) ||
       (r = check_group(name, c, qr.n_heads)) || (r = check_items(name, b.n_rows, qr.n_heads)) ||
       (r = check_select(name, n_select)))
@@ -371,7 +373,7 @@ int ibp_kv_select_workspace(const ibp_kv_cache* cache, const ibp_kv_batch* batch
   ibp::kv::Cache c;
   ibp::kv::Batch b;
   int r;
-  if ((r = check_cache(name, cache, false, &c)) || (r = check_batch(name, batch, c, false, &b)) ||
+  if ((r = check_cache(name, cache, false, &c)) || (r = check_batch(name, batch, c, false, true, &b)) ||
       (r = check_items(name, b.n_rows, c.n_heads)) || (r = check_select(name, n_select)))
     return r;
   *bytes = ibp::kv::select_workspace(c, b, n_select);

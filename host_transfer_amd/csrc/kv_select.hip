@@ -514,7 +514,8 @@ hipError_t run_select(const Cache& c, const Batch& b, const void* bounds, uint32
     while ((1u << padded_log2) < group && padded_log2 < 4) ++padded_log2;
     const uint32_t rows = 16u >> padded_log2;
     const uint32_t tiles = (b.max_q + rows - 1) / rows;
-    const uint64_t blocks = (uint64_t)b.n_seqs * tiles * (sc.pages / kScorePages) * c.n_heads;
+    uint64_t blocks = (uint64_t)b.n_seqs * tiles;  // (its factors: below 2^24, 2^23 and 2^16)
+    if (blocks <= 0xFFFFFFull) blocks *= (uint64_t)(sc.pages / kScorePages) * c.n_heads;
     if (blocks > 0xFFFFFFull) return hipErrorInvalidConfiguration;
 #define IBP_KV_SCORE(DP)                                                                            \
   hipLaunchKernelGGL((k_kv_score<T, DP>), dim3((uint32_t)blocks), dim3(256), 0, s, c, b,            \

@@ -337,6 +337,27 @@ def test_attend_scale_zero():
         K.check_attention(c, out, lse, K.attention(c, 0.0), f"scale 0, {q_len} rows")
 
 
+def test_max_q_far_above_the_rows():
+    """max_q only has to be at least the new tokens of a sequence: a bound far above them is none of
+    the launch's size."""
+    c = K.Case([(1, 100), (30, 333), (2, 9)], dtype=BF16, d=64, h=2, group=3, page=16)
+    hq, n_select = c.h * c.group, 5
+    sel = K.select(c, K.all_bounds(c), 1, 1, n_select)
+    for max_q in (33, 1 << 20, (1 << 31) - 1):
+        log(f"max_q {max_q}")
+        out, lse = run_attend(c, 0.125, max_q=max_q)
+        K.check_attention(c, out, lse, K.attention(c, 0.125), f"max_q {max_q}")
+        k, v = c.pools()
+        cache, batch = kv.Cache(k, v), gpu_batch(c, max_q=max_q)
+        got = torch.full((c.n, c.h, n_select), -7, dtype=torch.int32, device="cuda")
+        bounds = K.all_bounds(c).cuda()
+        kv.select(cache, batch, bounds, c.wide_q.cuda()[:, :hq], got, n_first=1, n_last=1,
+                  workspace=ws(kv.select_workspace(cache, batch, c.n, n_select)))
+        kv.page_bounds(cache, batch, bounds)
+        torch.cuda.synchronize()
+        assert torch.equal(got.cpu(), sel.int()), f"max_q {max_q}"
+
+
 # ---------------------------------------------------------------- selection
 
 SEL_LENS = [(1, 1), (1, 500), (0, 0), (7, 333), (1, 16), (3, 17), (1, 999), (2, 1), (40, 260)]
