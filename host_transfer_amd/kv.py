@@ -94,6 +94,15 @@ def _on_device(name, t, dtype, dev):
                          f"{name}: on device {d}, not on the current one")
 
 
+def _current(cache, batch=None):
+    """The current device; the tensors of the cache and of the batch must be on it."""
+    dev = _device()
+    for name, x in (("cache", cache), ("batch", batch)):
+        if x is not None and x.device is not None and x.device != dev:
+            raise ValueError(f"{name}: on device {x.device}, not on the current one")
+    return dev
+
+
 def _strides(t):
     """Strides, those of axes of size 1 as if packed (they address nothing)."""
     if 1 not in t.shape:
@@ -138,7 +147,7 @@ class Cache:
         n_pages, page_tokens, n_heads, head_dim = k.shape
         self._set(k.data_ptr(), v.data_ptr(), n_pages, page_tokens, n_heads, head_dim,
                   _DTYPES[k.dtype], *s[:3])
-        self.k, self.v, self.torch_dtype = k, v, k.dtype
+        self.k, self.v, self.torch_dtype, self.device = k, v, k.dtype, dev
 
     @classmethod
     def from_pointers(cls, k, v, n_pages, page_tokens, n_heads, head_dim, dtype, page_stride=None,
@@ -150,7 +159,7 @@ class Cache:
         page_stride = page_tokens * token_stride if page_stride is None else page_stride
         self._set(ibp._ptr(k), ibp._ptr(v), n_pages, page_tokens, n_heads, head_dim, dtype,
                   page_stride, token_stride, head_stride)
-        self.k, self.v, self.torch_dtype = k, v, None
+        self.k, self.v, self.torch_dtype, self.device = k, v, None, None
         return self
 
     def _set(self, k, v, n_pages, page_tokens, n_heads, head_dim, dtype, *strides):
@@ -176,8 +185,9 @@ class Batch:
 
     def __init__(self, q_start, kv_len, page_table, max_q, max_kv):
         n = kv_len.numel()
+        self.device = _device()
         for name, t in (("q_start", q_start), ("kv_len", kv_len), ("page_table", page_table)):
-            _on_device(name, t, torch.int32, _device())
+            _on_device(name, t, torch.int32, self.device)
         if q_start.dim() != 1 or kv_len.dim() != 1 or q_start.numel() != n + 1 or \
                 not q_start.is_contiguous() or not kv_len.is_contiguous():
             raise ValueError("q_start must be (n_seqs + 1,), kv_len (n_seqs,), both contiguous")
@@ -192,7 +202,7 @@ class Batch:
     @classmethod
     def from_pointers(cls, q_start, kv_len, page_table, table_stride, n_seqs, max_q, max_kv):
         self = cls.__new__(cls)
-        self.pages = None
+        self.pages = self.device = None
         self._keep = (q_start, kv_len, page_table)
         self._set(ibp._ptr(q_start), ibp._ptr(kv_len), ibp._ptr(page_table), table_stride, n_seqs,
                   max_q, max_kv)
@@ -265,7 +275,7 @@ def append(cache, k, v, slots, q=None, q_out=None, positions=None, rope=None, fl
            k_norm=None, eps=1e-6, n_tokens=None, n_positions=None, rope_dim=None, stream=None):
     """k, v, q, q_out: (tokens, heads, head_dim) tensors or Rows (n_tokens is then needed); rope:
     float32 (n_positions, rope_dim), cosines then sines; slots, positions: int64 (tokens,)."""
-    dev = _device()
+    dev = _current(cache)
     kr, n = _rows("k", cache, k, n_tokens, dev)
     vr, _ = _rows("v", cache, v, n, dev)
     qr = None if q is None else _rows("q", cache, q, n, dev)[0]
@@ -284,7 +294,7 @@ def append(cache, k, v, slots, q=None, q_out=None, positions=None, rope=None, fl
 
 def page_bounds(cache, batch, bounds, stream=None):
     """bounds: (n_pages, n_heads, 2, head_dim) of the cache's dtype."""
-    dev = _device()
+    dev = _current(cache, batch)
     ibp._check(ibp._lib.ibp_kv_page_bounds(
         cache._c, batch._c(cache, 0),
         _of_dtype("bounds", cache, bounds, cache.n_pages * cache.n_heads * 2 * cache.head_dim, dev),
@@ -302,7 +312,7 @@ def attend(cache, batch, q, out, scale, window=0, flags=CAUSAL, lse=None, worksp
            n_rows=None, stream=None):
     """q, out: (rows, heads, head_dim) tensors or Rows (n_rows is then needed); lse: float32
     (rows, heads); workspace: a device tensor of at least attend_workspace() bytes."""
-    dev = _device()
+    dev = _current(cache, batch)
     qr, n = _rows("q", cache, q, n_rows, dev)
     orow, _ = _rows("out", cache, out, n, dev)
     ws, ws_bytes = _workspace(workspace, dev)
@@ -322,7 +332,7 @@ def select(cache, batch, bounds, q, sel, n_first=1, n_last=1, n_select=None, n_b
            workspace=None, n_rows=None, stream=None):
     """bounds: (n_bounds, n_heads, 2, head_dim) of the cache's dtype; sel: int32 (rows, n_heads,
     n_select)."""
-    dev = _device()
+    dev = _current(cache, batch)
     qr, n = _rows("q", cache, q, n_rows, dev)
     sel_p, n_select = _sel(sel, cache, n, n_select, dev)
     if isinstance(bounds, torch.Tensor):
@@ -347,7 +357,7 @@ def attend_selected_workspace(cache, batch, n_rows, n_q_heads, n_select) -> int:
 def attend_selected(cache, batch, q, sel, out, scale, lse=None, n_select=None, workspace=None,
                     n_rows=None, stream=None):
     """As attend (causal), over the pages that sel lists for each row and key head."""
-    dev = _device()
+    dev = _current(cache, batch)
     qr, n = _rows("q", cache, q, n_rows, dev)
     orow, _ = _rows("out", cache, out, n, dev)
     sel_p, n_select = _sel(sel, cache, n, n_select, dev)

@@ -28,6 +28,8 @@
  *     buffers described (what it means is said at each call).
  *   - A workspace is written by the call that it is given to; calls that may
  *     run at the same time (two streams, two graphs) need one each.
+ *   - What a call writes must not overlap what it reads, but where a call says
+ *     that it may.
  */
 #ifndef IBP_KV_H
 #define IBP_KV_H

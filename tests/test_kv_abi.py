@@ -197,6 +197,23 @@ def test_select_refusals(kv):
     refused(ibp.ERR_ALIGN, f, c, batch(kv), q, P + 2, o, 1.0, n_select=4, n_rows=3, stream=0)
 
 
+def test_cache_and_batch_on_another_device(kv):
+    """Tensors' owners remember their device: a call with another one current is refused."""
+    rows, out = kv.Rows(P, 128, 64, 2), kv.Rows(2 * P, 128, 64, 2)
+    for on in ("cache", "batch"):
+        c, b = cache(kv), batch(kv)
+        (c if on == "cache" else b).device = 99
+        calls = [lambda: kv.page_bounds(c, b, P, stream=0),
+                 lambda: kv.attend(c, b, rows, out, 1.0, n_rows=3, stream=0),
+                 lambda: kv.select(c, b, P, rows, P, n_select=4, n_bounds=9, n_rows=3, stream=0),
+                 lambda: kv.attend_selected(c, b, rows, P, out, 1.0, n_select=4, n_rows=3, stream=0)]
+        if on == "cache":
+            calls.append(lambda: kv.append(c, rows, rows, P, n_tokens=3, stream=0))
+        for call in calls:
+            with pytest.raises(ValueError, match=f"{on}: on device 99"):
+                call()
+
+
 def test_workspace_is_checked(kv):
     """A workspace that is too small or misaligned is refused (through the C call: the binding
     takes tensors only)."""
