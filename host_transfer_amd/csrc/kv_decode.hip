@@ -21,16 +21,17 @@ constexpr int kWaves = 4;
 //
 // Bound by the reading of K and V: 4 * D bytes a key against 4 * D * 16
 // operations of the matrix cores, 1/10 of their rate at the rate of HBM, so
-// that empty columns (a group smaller than 16 rows) cost nothing.  A lane
-// reads the same 16 B pieces of a K and of a V row (key l%16, pieces l/16 + 4i): the
-// page lookup of a lane serves both.  K goes from the registers into the
-// first product as it is; V passes through LDS (its wave's own part), where
-// the transposed read gives the second product's operand.  LDS rows are padded by
+// that empty columns (a group smaller than 16 rows) cost nothing.  Neighbouring lanes read
+// neighbouring pieces of a row, K as well as V: a load of 64 pieces then touches 8 lines.  (With K in
+// the first product's own order, 16 rows side by side, each load looked up 64, and the L1's
+// lookups bound what comes from L2: lists of 280 rows 196 against 155 us in all; from HBM
+// 300 against 291.)  Both pass through LDS, its wave's own part, K first, then V in its place:
+// the first product reads rows, the second one transposed.  LDS rows are padded by
 // 32 B: the eight rows that half a wave reads then lie in eight different 32 B
 // windows of the banks for every head_dim that is a multiple of 32.
 //
-// Measured (with the join): 20 sequences of up to 2,048 tokens, 40 heads (814 MB) 162 us, 5.0 TB/s;
-// 4 sequences of up to 131,072 tokens, 32 query heads on 8 key heads (1.61 GB) 300 us, 5.4 TB/s, as
+// Measured (with the join): 20 sequences of up to 2,048 tokens, 40 heads (814 MB) 157 us, 5.2 TB/s;
+// 4 sequences of up to 131,072 tokens, 32 query heads on 8 key heads (1.61 GB) 291 us, 5.5 TB/s, as
 // a large copy runs; 8 rows' lists of 2,048 tokens (67 MB) 23 us.
 template <typename T, int DP, bool kSelected, int kHeads>
 __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q, Rows out,
@@ -39,9 +40,11 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
                                                    uint32_t window, bool causal,
                                                    uint32_t row_tiles, Partial part,
                                                    float* __restrict__ lse) {
-  constexpr int KS = DP / 32;   // products of the scores; 16 B pieces of a lane and row
+  constexpr int KS = DP / 32;   // products of the scores
   constexpr int DT = DP / 16;   // tiles of the output
   constexpr int LD = DP + 16;   // LDS row, elements
+  constexpr int CH = DP / 8;    // 16 B pieces of a row
+  constexpr int RPL = kWave / CH, NL = kTile / RPL;  // rows of a load, loads of a tile
   constexpr int WORDS = kTile * LD / 2;  // of a wave; 16 rows of DP floats fit
   static_assert(16 * DP <= WORDS, "the end's exchange fits the V tiles");
   constexpr int kTurns = kWaves / kHeads;           // waves that share a key head
@@ -126,10 +129,9 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
   const T* vbase = (const T*)cache.v + (uint64_t)kh * cache.head_stride;
   T* sv = (T*)s_v[wave];
 
-  // the K and V rows of key t0 + 16 a + col, zeros where no row sees it; bit c of the
-  // result: some row sees key t0 + 16 a + c
-  auto locate = [&](int32_t t0, int a, const T*& kp, const T*& vp) -> uint32_t {
-    int32_t j = t0 + a * 16 + (int32_t)col;
+  // where key t0 + lane % 32 lies (elements); bit r of the result: some row sees key t0 + r
+  auto locate = [&](int32_t t0, uint64_t& at) -> uint32_t {
+    int32_t j = t0 + (int32_t)(lane % kTile);
     bool see = j < end;
     if (kSelected) {
       int32_t pg = -1;
@@ -150,65 +152,69 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
       id = table[page];
     }
     see = id >= 0 && (uint32_t)id < cache.n_pages;
-    const uint64_t at = (uint64_t)(uint32_t)id * cache.page_stride +
-                        (uint64_t)((uint32_t)j - page * cache.page.d) * cache.token_stride;
-    kp = see ? kbase + at : zeros;
-    vp = see ? vbase + at : zeros;
-    return (uint32_t)__ballot(see) & 0xFFFFu;
+    at = see ? (uint64_t)(uint32_t)id * cache.page_stride +
+                   (uint64_t)((uint32_t)j - page * cache.page.d) * cache.token_stride
+             : 0;
+    return (uint32_t)__ballot(see);
   };
+  // this lane's piece of row load_row + i * RPL: its offset (elements) from the pool's base
+  const uint32_t load_row = lane / CH, load_c = lane % CH * 8;
+  auto offset = [&](uint64_t at, int i) -> uint64_t {
+    const int r = (int)load_row + i * RPL;
+    return (((uint64_t)(uint32_t)__shfl((int)(uint32_t)(at >> 32), r) << 32) |
+            (uint32_t)__shfl((int)(uint32_t)at, r)) + load_c;
+  };
+  auto loads = [&](uint32_t there, int i) {  // whether that row is there and has this piece
+    return ((there >> (load_row + i * RPL)) & 1u) && load_c < hd;
+  };
+  T* put_at = sv + load_row * LD + load_c;
+  const T* k_at = sv + col * LD + quarter * 8;
   // this lane's part of a transposed read of V
   const T* tr_at = sv + (4 * quarter + col / 4) * LD + 4 * (col % 4);
   bool odd = false;  // values that only some rows see and that are no numbers were left out
 
   for (int32_t t0 = begin + (int32_t)(wave / kHeads) * kTile; t0 < end; t0 += kBlockKeys) {
-    V8<T> kf[2][KS], vf[2][KS];
-    uint32_t there[2];
-    bool plain = true;
+    V8<T> kf[NL], vf[NL];
+    uint64_t at;
+    const uint32_t there = locate(t0, at);
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      const T *kp, *vp;
-      there[a] = locate(t0, a, kp, vp);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint32_t c = (k * 4 + quarter) * 8;
-        kf[a][k] = load_row8(c < hd ? kp + c : zeros);
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const uint32_t c = (k * 4 + quarter) * 8;
-        vf[a][k] = load_row8(c < hd ? vp + c : zeros);
-      }
-      plain = plain && there[a] == 0xFFFFu;
+    for (int i = 0; i < NL; ++i) {
+      const uint64_t from_base = offset(at, i);
+      const bool on = loads(there, i);
+      kf[i] = load_row8(on ? kbase + from_base : zeros);
+      vf[i] = load_row8(on ? vbase + from_base : zeros);
     }
     // every row sees every key of the tile?  (in lists, one row: `see` said all of it)
+    bool plain = there == ~0u;
     if (!kSelected) plain = plain && t0 >= lo_e && t0 + kTile <= hi_a;
 
+    // K to LDS, row = key of the tile
+#pragma unroll
+    for (int i = 0; i < NL; ++i) *(V8<T>*)(put_at + i * RPL * LD) = kf[i];
+    wave_sync();
     f32x4 sc[2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
       sc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < KS; ++k) sc[a] = mfma16(kf[a][k], qf[k], sc[a]);
+      for (int k = 0; k < KS; ++k)
+        sc[a] = mfma16(*(const V8<T>*)(k_at + a * 16 * LD + k * 32), qf[k], sc[a]);
     }
     settle(sc[0], sc[1]);
     if (!kSelected && !plain) {  // (a list has one row: what it does not see is zeros)
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const int32_t j = t0 + a * 16 + (int32_t)col;
-        if (j < lo_e || j >= hi_a)
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            odd = odd || any_odd<T>(vf[a][k]);
-            vf[a][k] = finite_part<T>(vf[a][k]);
-          }
+      for (int i = 0; i < NL; ++i) {
+        const int32_t j = t0 + (int32_t)load_row + i * RPL;
+        if (j < lo_e || j >= hi_a) {
+          odd = odd || any_odd<T>(vf[i]);
+          vf[i] = finite_part<T>(vf[i]);
+        }
       }
     }
-    // V to LDS, row = key of the tile
+    // V in its place
+    wave_sync();
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-        *(V8<T>*)(sv + (a * 16 + col) * LD + (k * 4 + quarter) * 8) = vf[a][k];
+    for (int i = 0; i < NL; ++i) *(V8<T>*)(put_at + i * RPL * LD) = vf[i];
 
     // lane's scores: keys t0 + 16 a + 4 quarter + r of its column's row
     float x[8];
@@ -222,7 +228,7 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const uint32_t kk = 4 * quarter + r;
-          bool see = (there[a] >> kk) & 1u;
+          bool see = (there >> (a * 16 + kk)) & 1u;
           if (!kSelected) {
             const int32_t j = t0 + a * 16 + (int32_t)kk;
             see = see && j >= lo && j < hi;
@@ -264,24 +270,24 @@ __global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q,
     for (int32_t t0 = begin + (int32_t)(wave / kHeads) * kTile; t0 < end; t0 += kBlockKeys) {
       if (t0 >= lo_e && t0 + kTile <= hi_a) continue;
       V8<T> sees;
+      uint64_t at;
+      const uint32_t there = locate(t0, at);
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        const T *kp, *vp;
-        const uint32_t there = locate(t0, a, kp, vp);
-        const int32_t mine = t0 + a * 16 + (int32_t)col;
+      for (int i = 0; i < NL; ++i) {
+        const int32_t mine = t0 + (int32_t)load_row + i * RPL;
         const bool some = mine < lo_e || mine >= hi_a;
+        const uint64_t from_base = offset(at, i);
+        *(V8<T>*)(put_at + i * RPL * LD) =
+            odd_code<T>(load_row8(some && loads(there, i) ? vbase + from_base : zeros));
+      }
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const uint32_t c = (k * 4 + quarter) * 8;
-          *(V8<T>*)(sv + (a * 16 + col) * LD + c) =
-              odd_code<T>(load_row8(some && c < hd ? vp + c : zeros));
-        }
+      for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int32_t j = t0 + a * 16 + (int32_t)(4 * quarter) + r;
-          sees[a * 4 + r] = (T)(((there >> (4 * quarter + r)) & 1u) && j >= lo && j < hi ? 1.f : 0.f);
+          sees[a * 4 + r] =
+              (T)(((there >> (a * 16 + 4 * quarter + r)) & 1u) && j >= lo && j < hi ? 1.f : 0.f);
         }
-      }
       wave_sync();
 #pragma unroll
       for (int t = 0; t < DT; ++t) {
