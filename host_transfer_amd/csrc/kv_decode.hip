@@ -32,9 +32,12 @@ constexpr int kWaves = 4;
 //
 // Measured (with the join): 20 sequences of up to 2,048 tokens, 40 heads (814 MB) 157 us, 5.2 TB/s;
 // 4 sequences of up to 131,072 tokens, 32 query heads on 8 key heads (1.61 GB) 291 us, 5.5 TB/s, as
-// a large copy runs; 8 rows' lists of 2,048 tokens (67 MB) 23 us.
+// a large copy runs; 8 rows' lists of 2,048 tokens (67 MB) 23 us.  Lists are read from L2 as much as from
+// HBM and want three waves a SIMD (280 rows' lists 133 us in all with three, 155 with two, 172
+// with four, which spill); whole contexts two (131,072 tokens 291 us, 300 with three).  Loads of the next
+// tile issued while this one is computed made both slower (160 and 295 us).
 template <typename T, int DP, bool kSelected, int kHeads>
-__global__ __launch_bounds__(256) void k_kv_decode(Cache cache, Batch b, Rows q, Rows out,
+__global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_decode(Cache cache, Batch b, Rows q, Rows out,
                                                    const int32_t* __restrict__ sel,
                                                    uint32_t n_select, float scale_log2,
                                                    uint32_t window, bool causal,
