@@ -71,11 +71,11 @@ struct Scores {
 //
 // With q split into its positive and negative part the score is a product of [hi, lo] rows
 // with [q+, q-] columns for the matrix cores: max(q lo, q hi) = q+ hi + q- lo where all is
-// finite, and a lane reads the bounds as k_kv_decode reads K.  The magnitudes are the same
+// finite, the rows read and passed through LDS as k_kv_decode does.  The magnitudes are the same
 // product of absolute values.  So the bounds are read once, at the rate of memory, for
-// 16 vectors; 64-bit sums of all pages in the vector ALU took 40 against 25 us for 8 rows of 32
-// heads over up to 4,096 pages (100 MB of bounds), and 146 against 32 us where 280 rows share
-// two sequences' pages.
+// 16 vectors: 8 rows of 32 heads over up to 4,096 pages (100 MB of bounds) 22 us, 280 rows that share two
+// sequences' pages 26 us; with 16 pages' pieces side by side in a load 25 and 32 us; 64-bit sums of
+// all pages in the vector ALU took 40 and 146 us.
 template <typename T, int DP>
 __global__ __launch_bounds__(256) void k_kv_score(Cache cache, Batch b, const T* __restrict__ bounds,
                                                   uint32_t n_bounds, Rows q, uint32_t n_first,
@@ -83,7 +83,10 @@ __global__ __launch_bounds__(256) void k_kv_score(Cache cache, Batch b, const T*
                                                   uint32_t row_tiles, uint32_t padded_log2,
                                                   Scores out) {
   constexpr int KS = DP / 32;
+  constexpr int CH = DP / 8, RPL = kWave / (2 * CH), NL = 16 / RPL;  // pieces of a bound; loads
+  constexpr int LD = 2 * DP + 16;  // LDS row, elements (padded as k_kv_decode's)
   typedef V8<T> v8;
+  __shared__ __align__(16) uint32_t s_rows[4][16 * LD / 2];
   const uint32_t lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
   const uint32_t col = lane % 16, quarter = lane / 16;
   const uint32_t group = q.n_heads / cache.n_heads, hd = cache.head_dim;
@@ -139,17 +142,21 @@ __global__ __launch_bounds__(256) void k_kv_score(Cache cache, Batch b, const T*
   id = (int32_t)lane < kPages && id >= rg.lo && id < rg.hi ? table[id] : -1;
   const bool bounded = id >= 0 && (uint32_t)id < n_bounds;
   const uint64_t all_there = __ballot(bounded);
-  v8 lo[2][KS], hi[2][KS];
+  // A page's row is [lo, hi]; neighbouring lanes read its neighbouring pieces (k_kv_decode says why),
+  // which pass through LDS, the wave's own part, into the products' order.
+  const uint32_t load_row = lane / (2 * CH), part = lane / CH % 2, load_c = lane % CH * 8;
+  const bool live = load_c < hd;
+  T* put_at = (T*)s_rows[wave] + load_row * LD + part * DP + load_c;
+  const T* row_at = (const T*)s_rows[wave] + col * LD + quarter * 8;
+  v8 x[2][NL];
   auto load = [&](int a) {
-    const int from = a * 16 + (int)col;
-    const int32_t pid = __shfl(id, from);
-    const bool has = (all_there >> from) & 1u;
-    const T* at = has ? base + (uint64_t)(uint32_t)pid * page_size : zeros;
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const uint32_t c = (k * 4 + quarter) * 8;
-      lo[a % 2][k] = load_row8(c < hd ? at + c : zeros);
-      hi[a % 2][k] = load_row8(c < hd ? (has ? at + hd : at) + c : zeros);
+    for (int i = 0; i < NL; ++i) {
+      const int from = a * 16 + (int)load_row + i * RPL;
+      const int32_t pid = __shfl(id, from);
+      const bool has = (all_there >> from) & 1u;
+      x[a % 2][i] = load_row8(has && live ? base + (uint64_t)(uint32_t)pid * page_size + part * hd + load_c
+                                          : zeros);
     }
   };
   load(0);
@@ -158,27 +165,32 @@ __global__ __launch_bounds__(256) void k_kv_score(Cache cache, Batch b, const T*
 #pragma unroll
   for (int a = 0; a < kPages / 16; ++a) {
     if (a + 1 < kPages / 16) load(a + 1);
+#pragma unroll
+    for (int i = 0; i < NL; ++i) *(v8*)(put_at + i * RPL * LD) = x[a % 2][i];
+    wave_sync();
     const uint32_t there = (uint32_t)(all_there >> (16 * a));
     f32x4 sc, mag;
     for (uint32_t v0 = 0; v0 < group; v0 += 16) {  // one pass up to 16 heads a group
       if (group > 16) load_q(v0);
-      f32x4 x = f32x4{0.f, 0.f, 0.f, 0.f}, m = x;
+      f32x4 y = f32x4{0.f, 0.f, 0.f, 0.f}, m = y;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        x = mfma16(hi[a % 2][k], qp[k], x);
-        m = mfma16(absolute(hi[a % 2][k]), qp[k], m);
-        x = mfma16(lo[a % 2][k], qn[k], x);
-        m = mfma16(absolute(lo[a % 2][k]), qm[k], m);
+        const v8 lo = *(const v8*)(row_at + k * 32), hi = *(const v8*)(row_at + DP + k * 32);
+        y = mfma16(hi, qp[k], y);
+        m = mfma16(absolute(hi), qp[k], m);
+        y = mfma16(lo, qn[k], y);
+        m = mfma16(absolute(lo), qm[k], m);
       }
-      settle(x, m);
+      settle(y, m);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         // anything that is no number makes the magnitude infinite, and all scores are formed anew
-        const float y = m[r] == m[r] && x[r] == x[r] ? m[r] : INFINITY;
-        sc[r] = v0 ? fmaxf(sc[r], x[r]) : x[r];
-        mag[r] = v0 ? fmaxf(mag[r], y) : y;
+        const float z = m[r] == m[r] && y[r] == y[r] ? m[r] : INFINITY;
+        sc[r] = v0 ? fmaxf(sc[r], y[r]) : y[r];
+        mag[r] = v0 ? fmaxf(mag[r], z) : z;
       }
     }
+    wave_sync();
     // the largest over a row's vectors, in neighbouring columns
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
