@@ -19,6 +19,9 @@ namespace {
 //          or two (many rows: as many as it runs; more only add partial results to write and
 //          join, 2048 tokens of 32 heads 62 us with two, 74 with four), but no split below 256
 //          keys of a wave's turn (few) or 512.
+//   order  Where contexts are as long again as the chunks or longer, up to 64 sequences: the longest
+//          sequence's tiles first (k_kv_chunk; chunks of up to 511 over 9,001 to 2,701 tokens 280
+//          -> 250 us), else each sequence's last tiles first.
 // A window bounds the keys of a tile; the workspace is sized without one, for as many splits or
 // more.
 hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
@@ -42,6 +45,7 @@ hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_
   if (splits > kMaxSplits) splits = kMaxSplits;
   p->splits = splits < 1 ? 1 : (uint32_t)splits;
   p->blocks = base * p->splits;
+  p->by_length = !p->few && b.n_seqs > 1 && b.n_seqs <= (uint32_t)kWave && (uint64_t)b.max_q * 2 <= b.max_kv;
   // a launch's threads are counted in 32 bits: 256 a workgroup, up to 1024 a row where many
   // splits are joined
   const uint64_t units = (uint64_t)b.n_rows * n_q_heads;

@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 template <typename T, int DP, bool kExact>  // kExact: head_dim == DP == the LDS row
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     Cache cache, Batch b, Rows q, Rows out, float scale, uint32_t window, bool causal,
-    uint32_t row_tiles, Partial part, float* __restrict__ lse) {
+    uint32_t row_tiles, bool by_length, Partial part, float* __restrict__ lse) {
   constexpr int KS = DP / 16;                            // products of a score
   constexpr int DT = DP / 32;                            // tiles of the output
   constexpr int DL = DP <= 64 ? 64 : DP <= 128 ? 128 : 256;  // LDS row, elements
@@ -86,17 +86,39 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   const uint32_t hd = kExact ? DP : cache.head_dim;
 
   // block -> key head (innermost: blocks of one head meet in one XCD's L2 where the heads
-  // are a multiple of eight), split, sequence, row tile from the last (under a
+  // are a multiple of eight), split, then sequence, row tile from the last (under a
   // causal mask the longest)
   uint32_t u = blockIdx.x;
   const uint32_t kh = u % cache.n_heads;
   u /= cache.n_heads;
   const uint32_t split = u % part.splits;
   u /= part.splits;
-  const uint32_t s = u % b.n_seqs;
-  const uint32_t tile = row_tiles - 1 - u / b.n_seqs;
-
-  const Seq sq = load_seq(b, s);
+  uint32_t s, tile;
+  Seq sq;
+  if (!by_length) {
+    s = u % b.n_seqs;
+    tile = row_tiles - 1 - u / b.n_seqs;
+    sq = load_seq(b, s);
+  } else {
+    // Chunks against longer contexts, whose tiles' times differ by sequence more than inside
+    // one: the longest sequence's first (a lane per sequence), so that two long tiles seldom
+    // share a CU and none begins late.
+    Seq mine = Seq{0, 0, 0, 0};
+    if (lane < b.n_seqs) mine = load_seq(b, lane);
+    const uint32_t n_tiles = ((uint32_t)max(mine.q_len, 0) * group + kRows - 1) / kRows;
+    uint32_t before = 0, total = 0;
+    for (uint32_t j = 0; j < b.n_seqs; ++j) {
+      const int32_t keys = __builtin_amdgcn_readlane(mine.n_keys, j);
+      const uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)n_tiles, j);
+      if (keys > mine.n_keys || (keys == mine.n_keys && j < lane)) before += n;
+      total += n;
+    }
+    if (u >= total) return;
+    s = (uint32_t)__builtin_ctzll(__ballot(u >= before && u - before < n_tiles));
+    tile = (uint32_t)__builtin_amdgcn_readlane((int)(n_tiles - 1 - (u - before)), s);
+    sq = Seq{__builtin_amdgcn_readlane(mine.row0, s), __builtin_amdgcn_readlane(mine.q_len, s),
+             __builtin_amdgcn_readlane(mine.first, s), __builtin_amdgcn_readlane(mine.n_keys, s)};
+  }
   const uint32_t n_m = (uint32_t)max(sq.q_len, 0) * group;
   const uint32_t m0 = tile * kRows;
   if (m0 >= n_m) return;
@@ -477,7 +499,7 @@ hipError_t run_chunk(const AttendPlan& p, const Cache& c, const Batch& b, const 
                      const Rows& out, float scale, uint32_t window, bool causal, float* lse,
                      Partial part, hipStream_t s) {
   hipLaunchKernelGGL((k_kv_chunk<T, DP, kExact>), dim3((uint32_t)p.blocks), dim3(kThreads), 0, s, c, b, q,
-                     out, scale, window, causal, p.row_tiles, part, lse);
+                     out, scale, window, causal, p.row_tiles, p.by_length, part, lse);
   return hipGetLastError();
 }
 

@@ -190,6 +190,7 @@ struct AttendPlan {
   uint32_t row_tiles;  // of a sequence and key head (of a row and key head in lists)
   uint32_t heads;      // key heads of a workgroup of kv_decode.hip
   uint32_t splits;
+  bool by_length;      // kv_chunk.hip: the longest sequences' tiles first
   uint64_t blocks;
 };
 

@@ -276,6 +276,25 @@ def test_attend_large_scores():
     K.check_attention(c, out, lse, K.attention(c, 0.25), "rising")
 
 
+@pytest.mark.parametrize("n_seqs", [2, 64, 65, 200])
+def test_chunks_of_many_sequences(n_seqs):
+    """Chunks in any order of lengths, equal ones and empty ones among them; row tiles of up to three
+    to a sequence."""
+    g = torch.Generator().manual_seed(n_seqs)
+    kv_len = torch.randint(0, 130, (n_seqs,), generator=g)
+    kv_len[:2] = torch.tensor([520, 520])
+    if n_seqs > 2:
+        kv_len[-1], kv_len[5] = 400, 0
+    lens = [(min(int(x), int(torch.randint(0, 60, (), generator=g))), int(x)) for x in kv_len]
+    lens[0], lens[1] = (260, 520), (17, 520)
+    c = K.Case(lens, dtype=BF16, d=32, h=1, group=1, page=16, tail_rows=2)
+    for window in (0, 50):
+        log(f"chunks of {n_seqs} sequences, window {window}")
+        out, lse = run_attend(c, 0.2, window=window)
+        K.check_attention(c, out, lse, K.attention(c, 0.2, window=window), f"{n_seqs} sequences")
+        assert (out[-2:] == PAD).all() and (lse[-2:] == PAD).all()
+
+
 @pytest.mark.parametrize("q_len", [1, 2, 40])
 def test_attend_many_small_weights(q_len):
     """One large score and so many small ones that their sum counts, each below half of fp16's
