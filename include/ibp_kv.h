@@ -143,8 +143,8 @@ int ibp_kv_page_bounds(const ibp_kv_cache *cache, const ibp_kv_batch *batch, voi
  * position p of its sequence and head h, with K and V of head
  * h / (q->n_heads / cache->n_heads), over the positions j it sees:
  *     out = sum_j exp(s_j) V_j / sum_j exp(s_j),   s_j = scale * <q, K_j>
- *     lse = log(sum_j exp(s_j))   (-inf for a row that sees nothing; its
- *                                  out is zeros)
+ *     lse = log(sum_j exp(s_j))   (-inf for a row that sees nothing, or only
+ *                                  scores of -inf; its out is zeros)
  * Row r sees positions 0 .. kv_len-1 of its sequence, under IBP_KV_CAUSAL
  * those <= p, with window > 0 those > p - window.
  *   q, out     n_heads a multiple of the cache's, the same for both; out must

@@ -295,6 +295,29 @@ def test_chunks_of_many_sequences(n_seqs):
         assert (out[-2:] == PAD).all() and (lse[-2:] == PAD).all()
 
 
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_attend_all_scores_minus_infinity(q_len):
+    """A row that sees scores of -inf only is one that sees nothing; with one finite score that key
+    has all the weight."""
+    for finite in (None, 3):
+        c = K.Case([(q_len, 60), (q_len, 900)], dtype=BF16, d=64, h=1, group=2, page=16)
+        c.q[:, :, 0] = 1.0
+        c.k[:, :, :, 0] = -math.inf
+        if finite is not None:
+            for s in range(2):
+                c.k[int(c.table[s, 0]), finite, 0, 0] = 1.0
+        log(f"scores of -inf, {q_len} rows, finite at {finite}")
+        out, lse = run_attend(c, 0.125, causal=False)
+        if finite is None:
+            assert (out == 0).all() and (lse == -math.inf).all()
+        else:
+            for s in range(2):  # a weight of 1 times a value of the dtype: exact
+                rows = slice(int(c.q_start[s]), int(c.q_start[s + 1]))
+                v = c.v[int(c.table[s, 0]), finite, 0].cuda()
+                assert torch.equal(out[rows], v.expand_as(out[rows]))
+                assert torch.isfinite(lse[rows]).all()
+
+
 @pytest.mark.parametrize("q_len", [1, 2, 40])
 def test_attend_many_small_weights(q_len):
     """One large score and so many small ones that their sum counts, each below half of fp16's
