@@ -99,7 +99,8 @@ __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp
 
 // The base that a row's exponents are taken against follows the row's largest score so far at a
 // distance: it is raised, to kLift below that score, when the score passes it by kRoom, so that
-// few steps rescale what was summed before them.  The largest weight lies between 2^kLift
+// few steps of k_kv_chunk rescale what was summed before them (k_kv_decode, whose vector ALU has
+// time, raises it with every new maximum).  The largest weight lies between 2^kLift
 // and 2^kRoom, where its rounding is as exact as near 1.  bf16 has the range of fp32.  fp16 has none below
 // 2^-24 and its full precision only from 2^-14 up: with its weights near the type's upper end
 // 2^-26 of the largest one still has all of it, and what is lost of n smaller ones is below n * 2^-37
