@@ -45,7 +45,8 @@ hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_
   if (splits > kMaxSplits) splits = kMaxSplits;
   p->splits = splits < 1 ? 1 : (uint32_t)splits;
   p->blocks = base * p->splits;
-  p->by_length = !p->few && b.n_seqs > 1 && b.n_seqs <= (uint32_t)kWave && (uint64_t)b.max_q * 2 <= b.max_kv;
+  p->by_length = !p->few && b.n_seqs > 1 && b.n_seqs <= (uint32_t)kWave &&
+                 (uint64_t)b.max_q * 2 <= b.max_kv;
   // a launch's threads are counted in 32 bits: 256 a workgroup, up to 1024 a row where many
   // splits are joined
   const uint64_t units = (uint64_t)b.n_rows * n_q_heads;

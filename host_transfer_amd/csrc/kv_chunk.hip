@@ -62,8 +62,9 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // 2.09 ms, 1.05 PFLOP/s, where a library product of 16,384^3 reaches 1.31 on the same card; the
 // matrix cores are busy 52 % of the time, the vector ALU 56 %, at the 1.9 GHz that power
 // leaves.  Without the pipeline (rows through registers, scores, weights and values in turn) it
-// took 2.49 ms.  No faster: 64 rows a wave, one wave a SIMD (2.09 ms; ragged chunks 380 against 290
-// us), half of the weights beside the values instead of the scores (the same).
+// took 2.49 ms.  Ragged chunks of up to 511 rows over 9,001 to 2,701 tokens 250 us, 840 TFLOP/s.
+// No faster: 64 rows a wave, one wave a SIMD (2.09 ms; ragged chunks 380 us where this then took
+// 290), half of the weights beside the values instead of the scores (the same).
 template <typename T, int DP, bool kExact>  // kExact: head_dim == DP == the LDS row
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     Cache cache, Batch b, Rows q, Rows out, float scale, uint32_t window, bool causal,

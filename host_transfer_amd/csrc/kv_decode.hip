@@ -32,17 +32,15 @@ constexpr int kWaves = 4;
 //
 // Measured (with the join): 20 sequences of up to 2,048 tokens, 40 heads (814 MB) 157 us, 5.2 TB/s;
 // 4 sequences of up to 131,072 tokens, 32 query heads on 8 key heads (1.61 GB) 291 us, 5.5 TB/s, as
-// a large copy runs; 8 rows' lists of 2,048 tokens (67 MB) 23 us.  Lists are read from L2 as much as from
-// HBM and want three waves a SIMD (280 rows' lists 133 us in all with three, 155 with two, 172
+// a large copy runs; 8 rows' lists of 2,048 tokens (67 MB) 22 us.  Lists come from L2 more than from HBM
+// and want three waves a SIMD (280 rows' lists 133 us in all with three, 155 with two, 172
 // with four, which spill); whole contexts two (131,072 tokens 291 us, 300 with three).  Loads of the next
 // tile issued while this one is computed made both slower (160 and 295 us).
 template <typename T, int DP, bool kSelected, int kHeads>
-__global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_decode(Cache cache, Batch b, Rows q, Rows out,
-                                                   const int32_t* __restrict__ sel,
-                                                   uint32_t n_select, float scale_log2,
-                                                   uint32_t window, bool causal,
-                                                   uint32_t row_tiles, Partial part,
-                                                   float* __restrict__ lse) {
+__global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_decode(
+    Cache cache, Batch b, Rows q, Rows out, const int32_t* __restrict__ sel, uint32_t n_select,
+    float scale_log2, uint32_t window, bool causal, uint32_t row_tiles, Partial part,
+    float* __restrict__ lse) {
   constexpr int KS = DP / 32;   // products of the scores
   constexpr int DT = DP / 16;   // tiles of the output
   constexpr int LD = DP + 16;   // LDS row, elements
@@ -258,7 +256,8 @@ __global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_deco
     V8<T> p;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-#pragma clang fp contract(off)  // (the product rounded as the base was: huge scores stay at most kRoom above)
+// (the product rounded as the base was: huge scores, too, stay at most kLift above it)
+#pragma clang fp contract(off)
       const float y = exp2_raw(x[e] - base);
       z += y;
       p[e] = (T)y;  // half a step of the dtype, relative, as the output's own rounding
@@ -331,7 +330,8 @@ __global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_deco
     zz += f[a] * s_z[mine + a * kHeads][r];
   }
   const uint32_t rm = m0 + r;
-  const uint32_t rrow = (uint32_t)(sq.row0 + i0) + rm / group, rhead = (kh - wave % kHeads + mine) * group + rm % group;
+  const uint32_t rrow = (uint32_t)(sq.row0 + i0) + rm / group;
+  const uint32_t rhead = (kh - wave % kHeads + mine) * group + rm % group;
   const uint64_t unit = (uint64_t)rrow * q.n_heads + rhead;
   const bool whole = part.splits == 1;
   const float inv = whole ? (zz == 0.f ? 0.f : 1.f / zz) : 1.f;
