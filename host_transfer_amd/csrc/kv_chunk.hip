@@ -338,6 +338,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   f32x16 sa[2], sb[2];
   if (begin < end) {
     scores(s_k[0], sa);
+    // The first step loads into s_k[0] at once: every wave has to have read it.
+    lds_barrier();
     settle(sa[0], sa[1]);
     float most = -INFINITY;
 #pragma unroll
@@ -346,7 +348,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   }
 
   // Step t0 (its scores in `cur`, masked, the base set; K of t0 + 64 and V of t0 in LDS):
-  // buffer `buf` holds V of t0 and gets K of t0 + 128, the other one gets V of t0 + 64.
+  // buffer `buf` holds V of t0 and gets K of t0 + 128, the other one gets V of t0 + 64.  Both loads
+  // begin on entry, so a barrier lies between it and the last reading of s_k[buf] (the scores of t0,
+  // in the step before or ahead of the loop) and of s_v[buf ^ 1] (the values of t0 - 64).
   auto step = [&](int32_t t0, uint32_t buf, f32x16 (&cur)[2], f32x16 (&nxt)[2]) {
     seen2 = locate(t0 + 2 * kKeys, id2, at2);
     if (t0 + kKeys < end) bring(vbase, at1, seen1, lds_v + (buf ^ 1) * TILE * 2, false);

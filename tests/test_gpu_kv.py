@@ -295,6 +295,36 @@ def test_chunks_of_many_sequences(n_seqs):
         assert (out[-2:] == PAD).all() and (lse[-2:] == PAD).all()
 
 
+@pytest.mark.parametrize("dtype,d,page", [(BF16, 128, 16), (F16, 64, 64), (BF16, 80, 24), (F16, 256, 16)])
+def test_chunk_first_keys_of_a_long_context(dtype, d, page):
+    """The first 64 keys of a chunk's context have most of the weight, and their place in LDS is the
+    first that later keys take.  200 sequences that share their pages and have the same queries, two
+    workgroups or more to each CU: the same bits for every sequence and every call, and the
+    formula's values."""
+    q_len, n, copies = 70, 1300, 200
+    c = K.Case([(q_len, n)], dtype=dtype, h=2, group=2, d=d, page=page, seed=d)
+    for j in range(64):  # (their scores are twice as far apart as the others')
+        c.k[int(c.table[0, j // page]), j % page] *= 2
+    log(f"first keys {dtype} d={d} page={page}")
+    k, v = c.pools()
+    cache, hq = kv.Cache(k, v), 4
+    start = torch.arange(copies + 1, dtype=torch.int32, device="cuda") * q_len
+    batch = kv.Batch(start, c.kv_len.cuda().expand(copies).contiguous(),
+                     c.table.cuda().expand(copies, -1).contiguous(), q_len, n)
+    q = c.wide_q.cuda()[:, :hq].repeat(copies, 1, 1)
+    w = ws(kv.attend_workspace(cache, batch, q.shape[0], hq))
+    for rep in range(3):
+        out = torch.full_like(q, PAD)
+        lse = torch.full(q.shape[:2], PAD, device="cuda")
+        kv.attend(cache, batch, q, out, 1 / math.sqrt(d), lse=lse, workspace=w)
+        torch.cuda.synchronize()
+        o, z = out.view(copies, q_len, hq, d), lse.view(copies, q_len, hq)
+        if rep == 0:
+            first = o[0].clone(), z[0].clone()
+            K.check_attention(c, *first, K.attention(c, 1 / math.sqrt(d)), "first keys")
+        assert (o == first[0]).all() and (z == first[1]).all(), rep
+
+
 @pytest.mark.parametrize("q_len", [1, 40])
 def test_attend_all_scores_minus_infinity(q_len):
     """A row that sees scores of -inf only is one that sees nothing; with one finite score that key
