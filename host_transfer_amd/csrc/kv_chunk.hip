@@ -79,7 +79,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   constexpr int TILE = kKeys * DL;
   __shared__ __align__(1024) uint16_t s_k[2][TILE];
   __shared__ __align__(1024) uint16_t s_v[2][TILE];
-  __shared__ uint32_t s_odd;
+  __shared__ uint32_t s_odd, s_bad;
 
   const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
   const uint32_t col = lane % 32, half = lane / 32;
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     const int32_t id0 = lookup(begin), id1 = lookup(begin + kKeys);
     seen0 = locate(begin, id0, at0);
     seen1 = locate(begin + kKeys, id1, at1);
-    if (tid == 0) s_odd = 0;
+    if (tid == 0) s_odd = s_bad = 0;
     lds_barrier();
     if (begin < end) {
       bring(kbase, at0, seen0, lds_k, true);
@@ -428,10 +428,11 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
 
   settle(o);
   if (odd) s_odd = 1;
+  if (probe(o) != 0.f) s_bad = 1;
   lds_barrier();
-  if (s_odd) {
+  if (s_odd || s_bad) {
     for (int32_t t0 = begin; t0 < end; t0 += kKeys) {
-      if (!is_edge(t0)) continue;
+      if (!s_bad && !is_edge(t0)) continue;
       uint64_t at;
       const uint64_t seen = locate(t0, lookup(t0), at);
       bring(vbase, at, seen, lds_v, false);
@@ -493,7 +494,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       const uint32_t c = t * 32 + 8 * r + 4 * half;
       t4 v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (T)(o[t][4 * r + e] * inv);
+      for (int e = 0; e < 4; ++e) v[e] = (T)mean(o[t][4 * r + e], inv);
       if (c < hd) *(t4*)(op + c) = v;
     }
   if (lse && half == 0) lse[unit] = z == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(z)) * kLn2;

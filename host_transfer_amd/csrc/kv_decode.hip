@@ -270,16 +270,17 @@ __global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_deco
   }
 
   settle(o);
-  if (!kSelected && __any(odd)) {
+  const bool all = __any(probe(o) != 0.f);  // (of every tile, else of those that some rows do not see)
+  if (all || __any(odd)) {
     for (int32_t t0 = begin + (int32_t)(wave / kHeads) * kTile; t0 < end; t0 += kBlockKeys) {
-      if (t0 >= lo_e && t0 + kTile <= hi_a) continue;
+      if (!all && t0 >= lo_e && t0 + kTile <= hi_a) continue;
       V8<T> sees;
       uint64_t at;
       const uint32_t there = locate(t0, at);
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const int32_t mine = t0 + (int32_t)load_row + i * RPL;
-        const bool some = mine < lo_e || mine >= hi_a;
+        const bool some = all || mine < lo_e || mine >= hi_a;
         const uint64_t from_base = offset(at, i);
         *(V8<T>*)(put_at + i * RPL * LD) =
             odd_code<T>(load_row8(some && loads(there, i) ? vbase + from_base : zeros));
@@ -289,8 +290,9 @@ __global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_deco
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int32_t j = t0 + a * 16 + (int32_t)(4 * quarter) + r;
-          sees[a * 4 + r] =
-              (T)(((there >> (a * 16 + 4 * quarter + r)) & 1u) && j >= lo && j < hi ? 1.f : 0.f);
+          bool see = (there >> (a * 16 + 4 * quarter + r)) & 1u;
+          if (!kSelected) see = see && j >= lo && j < hi;
+          sees[a * 4 + r] = (T)(see ? 1.f : 0.f);
         }
       wave_sync();
 #pragma unroll
@@ -334,7 +336,7 @@ __global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_deco
   const uint32_t rhead = (kh - wave % kHeads + mine) * group + rm % group;
   const uint64_t unit = (uint64_t)rrow * q.n_heads + rhead;
   const bool whole = part.splits == 1;
-  const float inv = whole ? (zz == 0.f ? 0.f : 1.f / zz) : 1.f;
+  const float inv = zz == 0.f ? 0.f : 1.f / zz;
   T* op = (T*)out.p + rrow * out.token_stride + (uint64_t)rhead * out.head_stride;
   for (uint32_t c = first_c; c < hd / 8; c += kRowThreads) {
     float y[8];
@@ -342,8 +344,11 @@ __global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_deco
     for (int e = 0; e < 8; ++e) {
       y[e] = 0.f;
 #pragma unroll
-      for (int a = 0; a < kTurns; ++a) y[e] += f[a] * ((const float*)s_v[mine + a * kHeads])[r * DP + c * 8 + e];
-      y[e] *= inv;
+      for (int a = 0; a < kTurns; ++a) {
+        const float x = ((const float*)s_v[mine + a * kHeads])[r * DP + c * 8 + e];
+        y[e] += kTurns == 1 ? x : scaled(x, f[a]);
+      }
+      if (whole) y[e] = mean(y[e], inv);
     }
     if (whole) {
       V8<T> v;
@@ -396,14 +401,14 @@ __global__ __launch_bounds__(256) void k_kv_join_few(Batch b, Rows out, Partial 
     const float f = exp2_raw(x[e].x - base);
     z += f * x[e].y;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] += f == 0.f ? 0.f : f * y[e][r];
+    for (int r = 0; r < 4; ++r) o[r] += scaled(y[e][r], f);
   }
   const float inv = z == 0.f ? 0.f : 1.f / z;
   if (live) {
     typedef T t4 __attribute__((ext_vector_type(4)));
     t4 v;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = (T)(o[r] * inv);
+    for (int r = 0; r < 4; ++r) v[r] = (T)mean(o[r], inv);
     *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
   }
   if (lse && c == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
@@ -464,7 +469,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(Batch b, Rows out, Par
       const float f = s_f[e];
       const f32x4 y = *(const f32x4*)(part.row(unit, e) + c);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] += f == 0.f ? 0.f : f * y[r];
+      for (int r = 0; r < 4; ++r) o[r] += scaled(y[r], f);
     }
   }
   s_o[tid] = o;
@@ -483,7 +488,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(Batch b, Rows out, Par
     typedef T t4 __attribute__((ext_vector_type(4)));
     t4 v;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = (T)(o[r] * inv);
+    for (int r = 0; r < 4; ++r) v[r] = (T)mean(o[r], inv);
     *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
   }
   if (lse && tid == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;

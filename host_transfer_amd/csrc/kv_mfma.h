@@ -133,11 +133,14 @@ __device__ __forceinline__ V8<T> load_row8(const T* p) {
 // (a NaN times a weight of zero is a NaN) reaches the product with the values.
 static __device__ const uint4 zero_row[IBP_KV_MAX_HEAD_DIM / 8] = {};
 
-// Infinities and NaNs among values that only some of a product's rows see.  Such a
-// value times the weight of zero of a row that does not see it is a NaN, so it stays
-// out of the product (finite_part), and a second product of its code with the
-// rows' visibility (1 or 0) counts, exactly for up to 127 keys, what each output sees:
-// +inf counts 1, -inf 128, NaN 16384 (add_odd).
+// Infinities and NaNs among values.  Whoever sees one has it in that channel, whatever its weight (which
+// may be rounded to zero, in one split of the keys and not in another): a NaN, or an infinity if it
+// meets no NaN and no other infinity.  Among keys that only some of a product's rows see, such a
+// value times the weight of zero of a row that does not see it would be a NaN, so it stays
+// out of the product (finite_part).  Elsewhere it goes in, and leaves no output finite that it
+// meets, since any weight times it is no number: probe() finds that at the end.  In both cases a second
+// product of the values' codes with the rows' visibility (1 or 0) counts, exactly for up to
+// 127 keys, what each output sees: +inf counts 1, -inf 128, NaN 16384 (add_odd).
 template <typename T>
 __device__ __forceinline__ V8<T> finite_part(V8<T> v) {
 #pragma unroll
@@ -154,13 +157,30 @@ __device__ __forceinline__ V8<T> odd_code(V8<T> v) {
   }
   return v;
 }
+// A NaN of the products may stand for an infinity (times 0): what it is is counted here.  One that
+// was counted is 0x7FFFFFFF, whose low bits no product of 16-bit values leaves set.
 __device__ __forceinline__ float add_odd(float o, float count) {
   const uint32_t n = (uint32_t)count;
+  if (n == 0 || __float_as_uint(o) == 0x7FFFFFFFu) return o;
+  if (isnan(o)) o = 0.f;
   if (n & 127u) o += INFINITY;
   if ((n >> 7) & 127u) o -= INFINITY;
-  if (n >> 14) o = NAN;
-  return o;
+  return n >> 14 || isnan(o) ? __uint_as_float(0x7FFFFFFFu) : o;
 }
+// Not zero if one of the outputs is no number.
+template <typename V, int N>
+__device__ __forceinline__ float probe(const V (&o)[N]) {
+  float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+#pragma unroll
+    for (int r = 0; r < (int)(sizeof(V) / sizeof(float)); ++r) x[r % 4] = fmaf(o[t][r], 0.f, x[r % 4]);
+  return (x[0] + x[1]) + (x[2] + x[3]);
+}
+// A partial result times its factor, and an output from its sum of values and the inverse of its sum
+// of weights (0: there is no weight, the output is 0).
+__device__ __forceinline__ float scaled(float o, float factor) { return isfinite(o) ? o * factor : o; }
+__device__ __forceinline__ float mean(float o, float inv) { return inv == 0.f ? 0.f : o * inv; }
 template <typename T>
 __device__ __forceinline__ bool any_odd(V8<T> v) {
   bool odd = false;

@@ -154,6 +154,9 @@ int ibp_kv_page_bounds(const ibp_kv_cache *cache, const ibp_kv_batch *batch, voi
  *   workspace  ibp_kv_attend_workspace() bytes, 16 B aligned (NULL if 0).
  * Scores, the softmax and the sums are in 32 bits; the weights exp(s - max)
  * are rounded to the cache's dtype where they multiply V.
+ * A NaN or infinite value of V reaches that channel of every row that sees its
+ * token, however small the weight, one of zero too: as a NaN, or as the infinity
+ * where no NaN and no other infinity meets it.  A score that is NaN or +inf makes its row NaN.
  * Errors: NULL pointer; sizes (workspace too small; a grid past the
  * hardware's limits); alignment; unknown flags; scale not finite or past 2^126.
  */

@@ -276,6 +276,53 @@ def test_attend_large_scores():
     K.check_attention(c, out, lse, K.attention(c, 0.25), "rising")
 
 
+def n_splits(c, max_kv=None):
+    """Into how many parts a call splits each row's keys: its workspace has head_dim + 2 floats of each."""
+    k, v = c.pools()
+    hq = c.h * c.group
+    need = kv.attend_workspace(kv.Cache(k, v), gpu_batch(c, max_kv=max_kv), c.n, hq)
+    return need // (c.n * hq * (c.d + 2) * 4)
+
+
+@pytest.mark.parametrize("q_len,h,group", [(1, 1, 2), (1, 4, 3), (3, 2, 4), (2, 8, 1), (40, 1, 2), (70, 4, 1)])
+def test_attend_values_out_of_range_in_any_split(q_len, h, group):
+    """NaN and infinite values whose weight rounds to zero in 32 bits (scores 200 below the largest),
+    in the largest score's split, in others and in masked places: the same result wherever the keys are
+    split, and the formula's.  Few rows and chunks; without a split, few of them and many."""
+    n, d, page = 1500, 16, 16
+    for max_kv in (None, 9000, 90000):
+        c = K.Case([(q_len, n), (q_len, 700)], dtype=BF16, d=d, h=h, group=group, page=page, seed=q_len)
+        if max_kv:
+            c.table = torch.cat([c.table, torch.full((2, max_kv // page + 1), -1, dtype=torch.int32)], 1)
+        c.q[..., 0], c.k[..., 0] = 1.0, 0.0
+        at = lambda s, j: (int(c.table[s, j // page]), j % page)
+        for s, j in ((0, 777), (1, 3)):  # the largest scores: a value of 200 above the others
+            c.k[at(s, j)][:, 0] = 200.0
+        odd = {5: math.nan, 70: math.inf, 760: -math.inf, 780: math.inf, 1100: math.nan, n - 1: -math.inf,
+               n - 2: math.nan, n - 30: math.inf, 698: math.inf}
+        for i, (j, val) in enumerate(odd.items()):  # a channel each, and one that meets both infinities
+            for s in range(2):
+                if j < c.lens[s][1]:
+                    c.v[at(s, j)][:, i + 1] = val
+                    if val == math.inf or j == 760:
+                        c.v[at(s, j)][:, 12] = val
+        splits = n_splits(c, max_kv)
+        log(f"out of range in {splits} splits, q={q_len} h={h} group={group}")
+        assert max_kv is None or splits > (8 if max_kv == 90000 else 1)
+        for causal, window in ((False, 0), (True, 0), (True, 500)):
+            out, lse = run_attend(c, 1.0, causal, window, max_kv=max_kv)
+            K.check_attention(c, out, lse, K.attention(c, 1.0, causal=causal, window=window),
+                              f"{splits} splits, causal={causal} window={window}")
+        if max_kv is None and q_len <= 3:
+            sel = torch.arange(94, dtype=torch.int32).expand(c.n, h, 94).contiguous()
+            out, lse = run_attend(c, 1.0, sel=sel)
+            K.check_attention(c, out, lse, K.attention(c, 1.0, sel=sel), "lists")
+    # no score above -inf: zeros, whatever the values
+    c.q[..., 0], c.k[..., 0] = 1.0, -math.inf
+    out, lse = run_attend(c, 1.0, False, max_kv=max_kv)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
 @pytest.mark.parametrize("n_seqs", [2, 64, 65, 200])
 def test_chunks_of_many_sequences(n_seqs):
     """Chunks in any order of lengths, equal ones and empty ones among them; row tiles of up to three
