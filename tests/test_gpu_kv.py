@@ -323,6 +323,72 @@ def test_attend_values_out_of_range_in_any_split(q_len, h, group):
     assert (out == 0).all() and (lse == -math.inf).all()
 
 
+def wider_table(c, max_kv):
+    """The case's page table with room for max_kv tokens; the pages past its own are not there."""
+    room = -(-max_kv // c.page)
+    if c.table.shape[1] < room:
+        more = torch.full((c.table.shape[0], room - c.table.shape[1]), -1, dtype=torch.int32)
+        c.table = torch.cat([c.table, more], 1)
+
+
+@pytest.mark.parametrize("dtype,d,h,group,page", [
+    (BF16, 64, 2, 2, 16), (F16, 128, 1, 4, 24), (BF16, 128, 2, 1, 64), (F16, 96, 1, 2, 16),
+    (BF16, 192, 1, 2, 16), (F16, 256, 1, 2, 32), (BF16, 40, 1, 4, 8)])
+def test_attend_chunks_in_splits(dtype, d, h, group, page):
+    """Chunks whose keys are split over workgroups, into few parts and into many: causal,
+    windowed and open masks, sequences that have no keys in most of the splits, a split whose pages are
+    all missing, rows behind the last sequence left as they were."""
+    c = K.Case([(50, 1500), (0, 0), (33, 700), (24, 1100), (1, 64), (60, 60)], dtype=dtype, d=d, h=h,
+               group=group, page=page, fill=math.nan, tail_rows=2, seed=d + group)
+    c.table[3, 512 // page:-(-768 // page)] = -1
+    c.table[0, 1200 // page] = c.n_pages
+    wider_table(c, 40000)
+    scale = 1 / math.sqrt(d)
+    for causal, window in ((True, 0), (True, 1000), (False, 0)):
+        ref = K.attention(c, scale, causal=causal, window=window)
+        for max_kv, least in ((1500, 2), (4200, 3), (9000, 9), (40000, 40)):
+            splits = n_splits(c, max_kv)
+            log(f"chunks in {splits} splits {dtype} d={d} h={h} group={group} {causal} {window}")
+            assert splits >= least
+            out, lse = run_attend(c, scale, causal, window, max_kv=max_kv)
+            K.check_attention(c, out, lse, ref, f"{splits} splits, causal={causal} window={window}")
+            assert (out[c.n - 2:] == PAD).all() and (lse[c.n - 2:] == PAD).all()
+
+
+@pytest.mark.parametrize("dtype,d,h,group,page", [
+    (BF16, 64, 4, 2, 16), (F16, 128, 8, 1, 16), (BF16, 128, 4, 4, 24), (F16, 40, 4, 3, 8),
+    (BF16, 192, 4, 2, 16), (F16, 256, 8, 2, 32), (BF16, 96, 12, 1, 1), (F16, 8, 4, 16, 64)])
+def test_attend_few_rows_of_four_heads(dtype, d, h, group, page):
+    """Caches whose heads are a multiple of four, one to four new tokens of a sequence: every mask,
+    pages that are not there, rows before the first token, with and without splits of the keys."""
+    most = min(4, 16 // group)
+    lens = [(min(q, most), n) for q, n in ((1, 1), (4, 3), (0, 0), (2, 64), (1, 65), (3, 200), (0, 31),
+                                           (4, 129), (1, 310), (2, 33))]
+    c = K.Case(lens, dtype=dtype, d=d, h=h, group=group, page=page, fill=math.nan, tail_rows=2, seed=d)
+    for s, j, bad in ((5, 40, -1), (5, 150, c.n_pages), (8, 300, 1 << 30), (7, 0, -(1 << 31))):
+        c.table[s, j // page] = bad
+    wider_table(c, 30000)
+    scale = 1 / math.sqrt(d)
+    for causal, window in ((True, 0), (True, 1), (True, 50), (False, 0)):
+        ref = K.attention(c, scale, causal=causal, window=window)
+        for max_kv in (60, 310, 5000, 30000) if (causal, window) == (True, 0) else (310, 30000):
+            if max_kv == 60:  # tokens past it are not read
+                small = K.Case([(q, min(n, 60)) for q, n in lens], dtype=dtype, d=d, h=h, group=group,
+                               page=page, seed=d)
+                small.k, small.v, small.q, small.table = c.k, c.v, c.q, c.table
+                small.n, small.n_pages, small.wide_q, small.lens = c.n, c.n_pages, c.wide_q, lens
+                keys = small.keys
+                small.keys = lambda s, upto=None: keys(s, 60)
+                want = K.attention(small, scale)
+            else:
+                want = ref
+            log(f"four heads {dtype} d={d} h={h} group={group} {causal} {window} max_kv={max_kv}: "
+                f"{n_splits(c, max_kv)} splits")
+            out, lse = run_attend(c, scale, causal, window, max_kv=max_kv)
+            K.check_attention(c, out, lse, want, f"causal={causal} window={window} max_kv={max_kv}")
+            assert (out[c.n - 2:] == PAD).all() and (lse[c.n - 2:] == PAD).all()
+
+
 @pytest.mark.parametrize("n_seqs", [2, 64, 65, 200])
 def test_chunks_of_many_sequences(n_seqs):
     """Chunks in any order of lengths, equal ones and empty ones among them; row tiles of up to three
@@ -814,6 +880,51 @@ def test_graph_of_a_prompt_chunk():
         c.q = q.cpu()
         c.lens = [(40, 700 - 100 * rep), (70, 300 - 115 * rep)]
         K.check_attention(c, got[0], got[1], K.attention(c, 0.125), f"chunk replay {rep}")
+
+
+def test_graph_and_streams_of_chunks_in_splits():
+    """Chunks whose keys are split over workgroups: captured and replayed with other lengths and inputs,
+    eager calls between, and on two streams at once, each with its workspace."""
+    c = K.Case([(40, 1800), (33, 1300)], dtype=BF16, d=128, h=2, group=2, page=16)
+    wider_table(c, 6000)
+    k, v = c.pools()
+    cache, batch = kv.Cache(k, v), gpu_batch(c, max_kv=6000)
+    q = c.wide_q.cuda()[:, :4].contiguous()
+    need = kv.attend_workspace(cache, batch, c.n, 4)
+    assert need > c.n * 4 * 8 * 130 * 4
+    works = [ws(need) for _ in range(3)]
+
+    def call(out, lse, work, **kw):
+        kv.attend(cache, batch, q, out, 0.09, lse=lse, workspace=work, **kw)
+    got, want = ([torch.zeros_like(q), torch.zeros((c.n, 4), device="cuda")] for _ in range(2))
+    call(*got, works[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    log("capture split chunks")
+    with torch.cuda.graph(graph):
+        call(*got, works[0])
+    for rep in range(3):
+        q.copy_(torch.randn_like(q))
+        batch._keep[1].copy_(torch.tensor([1800 - 500 * rep, 1300 - 600 * rep]))
+        call(*want, works[1])
+        torch.cuda.synchronize()
+        for t in got:
+            t.fill_(5)
+        for w in works[:1]:
+            w.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), rep
+        c.q, c.lens = q.cpu(), [(40, 1800 - 500 * rep), (33, 1300 - 600 * rep)]
+        K.check_attention(c, *got, K.attention(c, 0.09), f"replay {rep}")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.zeros_like(q), torch.zeros((c.n, 4), device="cuda")] for _ in range(6)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        call(*o, works[1 + i % 2], stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
 
 
 @pytest.mark.parametrize("q_len", [1, 50])
