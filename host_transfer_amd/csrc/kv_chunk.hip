@@ -494,7 +494,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       const uint32_t c = t * 32 + 8 * r + 4 * half;
       t4 v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (T)mean(o[t][4 * r + e], inv);
+      for (int e = 0; e < 4; ++e) v[e] = mean<T>(o[t][4 * r + e], inv);
       if (c < hd) *(t4*)(op + c) = v;
     }
   if (lse && half == 0) lse[unit] = z == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(z)) * kLn2;

@@ -348,12 +348,11 @@ __global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_deco
         const float x = ((const float*)s_v[mine + a * kHeads])[r * DP + c * 8 + e];
         y[e] += kTurns == 1 ? x : scaled(x, f[a]);
       }
-      if (whole) y[e] = mean(y[e], inv);
     }
     if (whole) {
       V8<T> v;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (T)y[e];
+      for (int e = 0; e < 8; ++e) v[e] = mean<T>(y[e], inv);
       *(V8<T>*)(op + c * 8) = v;
     } else {
       float* to_ = part.row(unit, split) + c * 8;
@@ -408,7 +407,7 @@ __global__ __launch_bounds__(256) void k_kv_join_few(Batch b, Rows out, Partial 
     typedef T t4 __attribute__((ext_vector_type(4)));
     t4 v;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = (T)mean(o[r], inv);
+    for (int r = 0; r < 4; ++r) v[r] = mean<T>(o[r], inv);
     *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
   }
   if (lse && c == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
@@ -488,7 +487,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_kv_join(Batch b, Rows out, Par
     typedef T t4 __attribute__((ext_vector_type(4)));
     t4 v;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = (T)mean(o[r], inv);
+    for (int r = 0; r < 4; ++r) v[r] = mean<T>(o[r], inv);
     *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
   }
   if (lse && tid == 0) lse[unit] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;

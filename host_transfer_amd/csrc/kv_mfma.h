@@ -177,10 +177,18 @@ __device__ __forceinline__ float probe(const V (&o)[N]) {
     for (int r = 0; r < (int)(sizeof(V) / sizeof(float)); ++r) x[r % 4] = fmaf(o[t][r], 0.f, x[r % 4]);
   return (x[0] + x[1]) + (x[2] + x[3]);
 }
-// A partial result times its factor, and an output from its sum of values and the inverse of its sum
-// of weights (0: there is no weight, the output is 0).
+// A partial result times its factor.
 __device__ __forceinline__ float scaled(float o, float factor) { return isfinite(o) ? o * factor : o; }
-__device__ __forceinline__ float mean(float o, float inv) { return inv == 0.f ? 0.f : o * inv; }
+// An output from its sum of values and the inverse of its sum of weights (0: there is no weight, the
+// output is 0).  A mean of T's numbers is none past T's largest one; what the weights' rounding adds could
+// make an infinity of it.
+template <typename T>
+__device__ __forceinline__ T mean(float o, float inv) {
+  constexpr float kMost = __is_same(T, _Float16) ? 65504.f : 0x1.FEp127f;
+  float x = inv == 0.f ? 0.f : o * inv;
+  if (isfinite(o)) x = x > kMost ? kMost : x < -kMost ? -kMost : x;  // (a NaN stays)
+  return (T)x;
+}
 template <typename T>
 __device__ __forceinline__ bool any_odd(V8<T> v) {
   bool odd = false;

@@ -511,6 +511,42 @@ def test_attend_fp16_huge_scores(q_len):
             assert ((lse[:, h].cpu().double() - want).abs() <= (128 + 16) * 2.0 ** -24 * want).all()
 
 
+@pytest.mark.parametrize("q_len,h", [(1, 1), (2, 4), (40, 2)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attend_values_at_the_ends_of_the_type(dtype, q_len, h):
+    """A mean of values is none above them: where all are fp16's largest, or in bf16 of a size whose
+    sum over the keys 32 bits hold, the output is that and not an infinity; in splits too, and over
+    lists."""
+    n, page = 100, 16
+    big = torch.finfo(F16).max if dtype == F16 else 2.0 ** 120
+    u = K.half_step(dtype)
+    for max_kv in (None, 9000):
+        c = K.Case([(q_len, n), (q_len, 63)], dtype=dtype, d=16, h=h, group=2, page=page, seed=q_len)
+        if max_kv:
+            wider_table(c, max_kv)
+        c.v[:] = big
+        c.v[..., 3], c.v[..., 4] = -big, 0.0
+        for kind in ("random", "rounded up"):
+            if kind != "random":
+                c.q[:], c.k[:] = 1.0, 0.0
+            if kind == "rounded up":  # all weights but one just above half a step: they gain nearly all of it
+                x = -math.log(2) + math.log1p(1.05 * u)
+                c.k[..., 0] = torch.tensor(x, dtype=dtype)
+                c.k[..., 1] = x - c.k[0, 0, 0, 0].double()
+            for s, (_, kv_n) in enumerate(c.lens):
+                for j in range(kv_n):
+                    if kind == "rounded up" and j == 0:
+                        c.k[int(c.table[s, 0]), 0] = 0.0
+            log(f"ends of the type {dtype} q={q_len} h={h} max_kv={max_kv} {kind}")
+            sel = torch.arange(7, dtype=torch.int32).expand(c.n, h, 7).contiguous()
+            for out, lse in (run_attend(c, 1.0, causal=False, max_kv=max_kv), run_attend(c, 1.0, sel=sel)):
+                o = out.cpu().double()
+                # the weights' rounding, the output's, and 100 terms in 32 bits
+                tol = (2 * u + 2 * (n + 8) * K.U32) * big
+                off = float((o - c.v[0, 0, 0].double()).abs().nan_to_num(math.inf).max())
+                assert off <= tol and bool(torch.isfinite(lse).all()), (kind, off)
+
+
 def test_attend_scale_zero():
     """All seen keys weigh the same; a query or key that is no number still makes its rows NaN."""
     for q_len in (1, 40):
