@@ -101,7 +101,8 @@ __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp
 // distance: it is raised, to kLift below that score, when the score passes it by kRoom, so that
 // few steps of k_kv_chunk rescale what was summed before them (k_kv_decode, whose vector ALU has
 // time, raises it with every new maximum).  The largest weight lies between 2^kLift
-// and 2^kRoom, where its rounding is as exact as near 1.  bf16 has the range of fp32.  fp16 has none below
+// and 2^kRoom, where its rounding is as exact as near 1.  bf16 has the range of fp32: weights up to 1, so
+// that sums of large values pass 2^128 no sooner than the values' own.  fp16 has none below
 // 2^-24 and its full precision only from 2^-14 up: with its weights near the type's upper end
 // 2^-26 of the largest one still has all of it, and what is lost of n smaller ones is below n * 2^-37
 // of the largest (with weights up to 1 it was n * 2^-25: 30,000 weights of 2^-25, 7.5e-4 of
@@ -115,7 +116,7 @@ struct Base<_Float16> {
 };
 template <>
 struct Base<__bf16> {
-  static constexpr float kLift = 0.f, kRoom = 8.f;
+  static constexpr float kLift = -8.f, kRoom = 0.f;
 };
 template <typename T>
 __device__ __forceinline__ float next_base(float base, float most) {

@@ -526,7 +526,7 @@ def test_attend_values_at_the_ends_of_the_type(dtype, q_len, h):
             wider_table(c, max_kv)
         c.v[:] = big
         c.v[..., 3], c.v[..., 4] = -big, 0.0
-        for kind in ("random", "rounded up"):
+        for kind in ("random", "rounded up", "rising"):
             if kind != "random":
                 c.q[:], c.k[:] = 1.0, 0.0
             if kind == "rounded up":  # all weights but one just above half a step: they gain nearly all of it
@@ -537,6 +537,8 @@ def test_attend_values_at_the_ends_of_the_type(dtype, q_len, h):
                 for j in range(kv_n):
                     if kind == "rounded up" and j == 0:
                         c.k[int(c.table[s, 0]), 0] = 0.0
+                    if kind == "rising" and j >= 64:  # 2^7.8 times the first keys' weights
+                        c.k[int(c.table[s, j // page]), j % page, :, 0] = 7.8 * math.log(2)
             log(f"ends of the type {dtype} q={q_len} h={h} max_kv={max_kv} {kind}")
             sel = torch.arange(7, dtype=torch.int32).expand(c.n, h, 7).contiguous()
             for out, lse in (run_attend(c, 1.0, causal=False, max_kv=max_kv), run_attend(c, 1.0, sel=sel)):
