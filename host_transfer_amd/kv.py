@@ -159,7 +159,8 @@ class Cache:
         page_stride = page_tokens * token_stride if page_stride is None else page_stride
         self._set(ibp._ptr(k), ibp._ptr(v), n_pages, page_tokens, n_heads, head_dim, dtype,
                   page_stride, token_stride, head_stride)
-        self.k, self.v, self.torch_dtype, self.device = k, v, None, None
+        self.k, self.v, self.device = k, v, None
+        self.torch_dtype = next((t for t, x in _DTYPES.items() if x == dtype), None)
         return self
 
     def _set(self, k, v, n_pages, page_tokens, n_heads, head_dim, dtype, *strides):
@@ -230,8 +231,7 @@ def _rows(name, cache, t, n_tokens, dev):
     shape = t.shape
     if len(shape) != 3 or shape[2] != cache.head_dim:
         raise ValueError(f"{name}: (tokens, heads, {cache.head_dim}) needed, got {tuple(shape)}")
-    if cache.torch_dtype is not None:
-        _on_device(name, t, cache.torch_dtype, dev)
+    _on_device(name, t, cache.torch_dtype, dev)
     n = shape[0]
     if n_tokens is not None and n != n_tokens:
         raise ValueError(f"{name}: {n_tokens} tokens needed, got {n}")
@@ -247,8 +247,6 @@ def _rows(name, cache, t, n_tokens, dev):
 
 
 def _of_dtype(name, cache, t, numel, dev):
-    if cache.torch_dtype is None:
-        return ibp._ptr(t)
     return _plain(name, t, cache.torch_dtype, numel, dev)
 
 

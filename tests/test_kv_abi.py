@@ -249,6 +249,31 @@ def test_tensors_are_checked(kv):
         kv.append(c, torch.zeros(3, 2, 32, dtype=torch.bfloat16), torch.zeros(3, 2, 64), P, stream=0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tensors_beside_a_cache_of_pointers_are_checked(kv, dtype):
+    """A cache given by addresses has a dtype all the same: rows, bounds and weights that are tensors
+    of another one, or in host memory, are refused like those beside a cache of tensors."""
+    c, b = cache(kv), batch(kv)
+    r, q, o = kv.Rows(P, 128, 64, 2), kv.Rows(P, 256, 64, 4), kv.Rows(2 * P, 256, 64, 4)
+    x, y = torch.zeros(3, 2, 64, dtype=dtype), torch.zeros(3, 4, 64, dtype=dtype)
+    bounds, w = torch.zeros(10, 2, 2, 64, dtype=dtype), torch.zeros(64, dtype=dtype)
+    calls = dict(k=lambda: kv.append(c, x, r, P, n_tokens=3, stream=0),
+                 v=lambda: kv.append(c, r, x, P, n_tokens=3, stream=0),
+                 q=lambda: kv.append(c, r, r, P, q=y, q_out=o, n_tokens=3, stream=0),
+                 q_out=lambda: kv.append(c, r, r, P, q=q, q_out=y, n_tokens=3, stream=0),
+                 k_norm=lambda: kv.append(c, r, r, P, k_norm=w, n_tokens=3, stream=0),
+                 q_norm=lambda: kv.append(c, r, r, P, q=q, q_out=o, q_norm=w, n_tokens=3, stream=0),
+                 bounds=lambda: kv.page_bounds(c, b, bounds, stream=0))
+    for call, name in ((lambda: kv.attend(c, b, y, o, 1.0, n_rows=3, stream=0), "q"),
+                       (lambda: kv.attend(c, b, q, y, 1.0, n_rows=3, stream=0), "out"),
+                       (lambda: kv.select(c, b, P, y, P, n_select=8, n_bounds=9, stream=0), "q"),
+                       (lambda: kv.select(c, b, bounds, q, P, n_select=8, n_rows=3, stream=0), "bounds"),
+                       (lambda: kv.attend_selected(c, b, y, P, o, 1.0, n_select=8, stream=0), "q"),
+                       *((f, n) for n, f in calls.items())):
+        with pytest.raises(ValueError, match=f"^{name}: "):
+            call()
+
+
 def test_valid_calls_without_a_device_report_a_hip_error(kv):
     """Valid calls that enqueue nothing (no tokens, no rows)."""
     from host_transfer_amd import ibp
