@@ -282,6 +282,8 @@ def append(cache, k, v, slots, q=None, q_out=None, positions=None, rope=None, fl
         if rope.dim() != 2:
             raise ValueError("rope must be (n_positions, rope_dim)")
         n_positions, rope_dim = rope.shape
+    elif ibp._ptr(rope) and (n_positions is None or rope_dim is None):
+        raise ValueError("n_positions and rope_dim are needed with a pointer")
     ibp._check(ibp._lib.ibp_kv_append(
         cache._c, kr, vr, qr, qo, _plain("slots", slots, torch.int64, n, dev),
         _plain("positions", positions, torch.int64, n, dev), n,
@@ -338,6 +340,8 @@ def select(cache, batch, bounds, q, sel, n_first=1, n_last=1, n_select=None, n_b
             raise ValueError(f"bounds: (pages, {cache.n_heads}, 2, {cache.head_dim}) needed, got "
                              f"{tuple(bounds.shape)}")
         n_bounds = bounds.shape[0]
+    elif n_bounds is None:
+        raise ValueError("n_bounds is needed with a pointer")
     ws, ws_bytes = _workspace(workspace, dev)
     ibp._check(ibp._lib.ibp_kv_select(
         cache._c, batch._c(cache, n), _of_dtype("bounds", cache, bounds, 0, dev), n_bounds, qr, n_first,

@@ -274,6 +274,17 @@ def test_tensors_beside_a_cache_of_pointers_are_checked(kv, dtype):
             call()
 
 
+def test_pointers_need_their_sizes(kv):
+    """A rotation table or bounds given by address without their length: refused, not taken as empty
+    (no token would be placed)."""
+    c, r, q = cache(kv), kv.Rows(P, 128, 64, 2), kv.Rows(P, 256, 64, 4)
+    for kw in (dict(rope_dim=64), dict(n_positions=9), {}):
+        with pytest.raises(ValueError, match="n_positions and rope_dim"):
+            kv.append(c, r, r, P, positions=P, rope=P, n_tokens=3, stream=0, **kw)
+    with pytest.raises(ValueError, match="n_bounds"):
+        kv.select(c, batch(kv), P, q, P, n_select=8, n_rows=3, stream=0)
+
+
 def test_valid_calls_without_a_device_report_a_hip_error(kv):
     """Valid calls that enqueue nothing (no tokens, no rows)."""
     from host_transfer_amd import ibp
