@@ -56,6 +56,29 @@ bool extent_fits(uint64_t tokens, uint64_t token_stride, uint64_t heads, uint64_
   return ((a + b) >> 62) == 0;
 }
 
+// Whether rows of a and of b, which have the same strides, share memory: some dt tokens and dh heads
+// apart two rows start less than a row apart.
+bool rows_overlap(const ibp::kv::Rows& a, const ibp::kv::Rows& b, uint64_t n_tokens, uint32_t head_dim) {
+  typedef __int128 wide;
+  if (n_tokens == 0) return false;
+  const wide d = ((wide)(uintptr_t)b.p - (wide)(uintptr_t)a.p) / 2;
+  const wide ts = n_tokens > 1 ? (wide)a.token_stride : 0, hs = a.head_stride, heads = a.n_heads;
+  const wide reach = ts * (n_tokens - 1) + hs * (heads - 1) + head_dim;
+  if (d >= reach || -d >= reach) return false;
+  for (wide dh = 1 - heads; dh < heads; ++dh) {
+    const wide rem = d + dh * hs;  // + dt * ts, the nearest to zero: one of two dt
+    const wide dt = ts ? -rem / ts : 0;
+    for (wide t = dt - 1; t <= dt + 1; ++t)
+      if (t > -(wide)n_tokens && t < (wide)n_tokens && rem + t * ts < head_dim && -(rem + t * ts) < head_dim)
+        return true;
+  }
+  return false;
+}
+
+bool same_strides(const ibp::kv::Rows& a, const ibp::kv::Rows& b) {
+  return a.token_stride == b.token_stride && a.head_stride == b.head_stride;
+}
+
 // pools: also require k and v (a call that reads neither passes false).
 int check_cache(const char* name, const ibp_kv_cache* c, bool pools, ibp::kv::Cache* out) {
   if (!c || (pools && (!c->k || !c->v)))
@@ -203,7 +226,7 @@ int attend(const char* name, const ibp_kv_cache* cache, const ibp_kv_batch* batc
     return r;
   if (orow.n_heads != qr.n_heads)
     return set_error(IBP_ERR_SIZE, "%s: out has %u heads, q has %u", name, orow.n_heads, qr.n_heads);
-  if (b.n_rows && orow.p == qr.p)
+  if (b.n_rows && (orow.p == qr.p || (same_strides(orow, qr) && rows_overlap(orow, qr, b.n_rows, c.head_dim))))
     return set_error(IBP_ERR_SIZE, "%s: out must not overlap q", name);
   if (!(fabsf(scale) <= 0x1p126f))  // (scores are in the exponent of 2: times 1.44)
     return set_error(IBP_ERR_SIZE, "%s: scale must be finite, its magnitude at most 2^126", name);
@@ -271,9 +294,10 @@ int ibp_kv_append(const ibp_kv_cache* cache, const ibp_kv_rows* k, const ibp_kv_
     if (qr.n_heads != qo.n_heads)
       return set_error(IBP_ERR_SIZE, "%s: q has %u heads, q_out has %u", name, qr.n_heads,
                        qo.n_heads);
-    if (n_tokens && qr.p == qo.p &&
-        (qr.token_stride != qo.token_stride || qr.head_stride != qo.head_stride))
+    if (n_tokens && qr.p == qo.p && !same_strides(qr, qo))
       return set_error(IBP_ERR_SIZE, "%s: q_out in place of q needs q's strides", name);
+    if (qr.p != qo.p && same_strides(qr, qo) && rows_overlap(qr, qo, n_tokens, c.head_dim))
+      return set_error(IBP_ERR_SIZE, "%s: q_out overlaps q without being q", name);
   }
   if (c.k == c.v)
     return set_error(IBP_ERR_SIZE, "%s: k and v of the cache are the same memory", name);

@@ -114,8 +114,8 @@ typedef struct {
  *              head's channels.  eps >= 0, finite.
  * The arithmetic is in 32 bits and is rounded once, at the end.
  * Errors: NULL pointer; sizes (rope_dim not a multiple of 16 or > head_dim,
- * head counts, n_tokens >= 2^31, rows of q_out that overlap, k and v of the
- * cache the same memory); alignment; flags.
+ * head counts, n_tokens >= 2^31, rows of q_out that overlap, q_out in part over
+ * q, k and v of the cache the same memory); alignment; flags.
  */
 #define IBP_KV_ROPE_INTERLEAVED 1u
 int ibp_kv_append(const ibp_kv_cache *cache, const ibp_kv_rows *k, const ibp_kv_rows *v,
@@ -148,7 +148,7 @@ int ibp_kv_page_bounds(const ibp_kv_cache *cache, const ibp_kv_batch *batch, voi
  * Row r sees positions 0 .. kv_len-1 of its sequence, under IBP_KV_CAUSAL
  * those <= p, with window > 0 those > p - window.
  *   q, out     n_heads a multiple of the cache's, the same for both; out must
- *              not overlap q.
+ *              not overlap q (refused where both have the same strides or start).
  *   lse        float[n_rows][q->n_heads] or NULL.
  *   window     0 = none; needs IBP_KV_CAUSAL (IBP_ERR_FLAGS).
  *   workspace  ibp_kv_attend_workspace() bytes, 16 B aligned (NULL if 0).

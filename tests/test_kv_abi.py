@@ -285,6 +285,30 @@ def test_pointers_need_their_sizes(kv):
         kv.select(c, batch(kv), P, q, P, n_select=8, n_rows=3, stream=0)
 
 
+def test_out_in_part_over_q(kv):
+    """out (or append's q_out) that starts inside q's rows is refused; slices of one buffer that lie
+    side by side are not."""
+    from host_transfer_amd import ibp
+    c, r = cache(kv), kv.Rows(P, 128, 64, 2)
+    ts = 1024  # elements, of a row of 16 slices of 64
+    bad = [64, -64, 128, 192, ts, -ts, ts + 64, 2 * ts - 64, 2 * ts + 192, 8, -8, 56, ts - 200, -2 * ts + 200]
+    good = [256, -256, 512, ts - 256, ts + 256, 3 * ts, 3 * ts + 64, -3 * ts - 192, 9 * ts]
+    # three tokens of four heads, and, the heads outermost, four tokens of three heads
+    for token_stride, head_stride, heads, tokens in ((ts, 64, 4, 3), (64, ts, 3, 4)):
+        q = kv.Rows(P, token_stride, head_stride, heads)
+        for d in bad + good:
+            o = kv.Rows(P + 2 * d, token_stride, head_stride, heads)
+            # what does not overlap is refused for eps and scale, so that nothing is enqueued
+            calls = [lambda: kv.append(c, r, r, P, q=q, q_out=o, n_tokens=tokens, eps=-1.0, stream=0)]
+            if heads == 4:  # (three are no multiple of the cache's two)
+                calls.append(lambda: kv.attend(c, batch(kv), q, o, float("nan"), n_rows=tokens, stream=0))
+            for call in calls:
+                with pytest.raises(ibp.IbpError) as e:
+                    call()
+                assert e.value.code == ibp.ERR_SIZE
+                assert ("overlap" in ibp.last_error()) == (d in bad), (d, heads, ibp.last_error())
+
+
 def test_valid_calls_without_a_device_report_a_hip_error(kv):
     """Valid calls that enqueue nothing (no tokens, no rows)."""
     from host_transfer_amd import ibp
