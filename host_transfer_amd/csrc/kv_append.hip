@@ -185,7 +185,7 @@ __device__ __forceinline__ T nan_max(T a, T b) {
 // 8 heads of 128 (114 MB) 27 us, 4.2 TB/s; two or four threads a piece 25 to 27 us.
 template <typename T>
 __global__ __launch_bounds__(256) void k_kv_page_bounds(Cache cache, Batch b, T* __restrict__ bounds,
-                                                        uint32_t pages_per_seq, uint32_t chunks) {
+                                                        uint32_t chunks) {
   const uint32_t s = blockIdx.y;
   const Seq q = load_seq(b, s);
   if (q.q_len <= 0) return;
@@ -242,7 +242,7 @@ hipError_t run_page_bounds(const Cache& c, const Batch& b, void* bounds, hipStre
     part.table += (uint64_t)s0 * b.table_stride;
     part.n_seqs = b.n_seqs - s0 < 65535 ? b.n_seqs - s0 : 65535;
     hipLaunchKernelGGL(k_kv_page_bounds<T>, dim3((uint32_t)blocks, part.n_seqs), dim3(256), 0, s,
-                       c, part, (T*)bounds, pages, chunks);
+                       c, part, (T*)bounds, chunks);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
