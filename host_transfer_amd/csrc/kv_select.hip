@@ -251,7 +251,7 @@ __device__ __forceinline__ uint32_t score_key32(float x) {
 // scored exactly and the best of them taken.  Selections are digit searches: histograms
 // of the candidates that agree in the digits so far, counted from the smallest one, so that
 // the first digit already spreads them over its bins.
-constexpr uint32_t kCachedPages = 12288;  // whose scores LDS holds (48 KB beside 9)
+constexpr uint32_t kCachedPages = 12288;  // whose scores LDS holds: 48 KB beside 11.4
 constexpr uint32_t kOpen = 256;            // open pages that are ranked one by one
 constexpr uint32_t kDigit = 11, kBins = 1u << kDigit;
 
@@ -270,6 +270,9 @@ __global__ __launch_bounds__(NT) void k_kv_pick(Cache cache, Batch b, const T* _
   __shared__ uint64_t s_key[kOpen];
   __shared__ int32_t s_page[kOpen];
   extern __shared__ float s_cached[];  // kCached: the scores of pages rg.lo ..
+  static_assert(!kCached || kCachedPages * sizeof(float) + sizeof(hist) + sizeof(s_lo) + sizeof(s_hi) +
+                                    sizeof(s_wave) + sizeof(s_key) + sizeof(s_page) + 64 <= 65536,
+                "the LDS that a workgroup has without asking for more");
   const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const uint32_t r = blockIdx.x / cache.n_heads, h = blockIdx.x % cache.n_heads;
   const int32_t s = seq_of_row(b, (int32_t)r);
