@@ -147,6 +147,11 @@ int ibp_kv_page_bounds(const ibp_kv_cache *cache, const ibp_kv_batch *batch, voi
  *                                  scores of -inf; its out is zeros)
  * Row r sees positions 0 .. kv_len-1 of its sequence, under IBP_KV_CAUSAL
  * those <= p, with window > 0 those > p - window.
+ * max_q decides how all sequences are run: where max_q times the query heads of a
+ * key head is above 16, single tokens beside a chunk are right but slow (512
+ * rows and 63 single tokens over up to 131,072 tokens 2.7 ms).  Two calls, over
+ * the sequences up to s and from s on (q_start + s, kv_len + s, page_table + s *
+ * table_stride; q, out and lse the same), are faster (0.9 ms).
  *   q, out     n_heads a multiple of the cache's, the same for both; out must
  *              not overlap q (refused where both have the same strides or start).
  *   lse        float[n_rows][q->n_heads] or NULL.
@@ -188,7 +193,11 @@ int ibp_kv_attend_workspace(const ibp_kv_cache *cache, const ibp_kv_batch *batch
  *             tokens too); n_first + n_last <= n_select <= IBP_KV_MAX_SELECT.
  *   sel       int32[n_rows][cache->n_heads][n_select], page numbers of the
  *             sequence in ascending order, then -1.
- *   workspace ibp_kv_select_workspace() bytes, 16 B aligned.
+ *   workspace ibp_kv_select_workspace() bytes, 16 B aligned: for each row and key
+ *             head about 12 for each of the ceil(max_kv / page_tokens) pages, rounded up
+ *             to 256 pages (none where n_select covers them all).  8,192 rows of 8
+ *             heads over 4,096 pages take 3.2 GB: a long prompt's rows are
+ *             best given some at a time, with the same sel and workspace.
  */
 int ibp_kv_select(const ibp_kv_cache *cache, const ibp_kv_batch *batch, const void *bounds,
                   uint64_t n_bounds, const ibp_kv_rows *q, uint32_t n_first, uint32_t n_last,
@@ -202,7 +211,9 @@ int ibp_kv_select_workspace(const ibp_kv_cache *cache, const ibp_kv_batch *batch
  * key head over the pages of its own list only.
  *   sel  as ibp_kv_select writes it: int32[n_rows][cache->n_heads][n_select].
  *        Entries outside [0, ceil(max_kv / page_tokens)), and one that is not
- *        above the entry before it, are passed over.
+ *        above the entry before it, are passed over.  (So a list in any other than
+ *        ascending order may name a page twice with a smaller entry between; its keys then
+ *        count twice.)
  */
 int ibp_kv_attend_selected(const ibp_kv_cache *cache, const ibp_kv_batch *batch,
                            const ibp_kv_rows *q, const ibp_kv_rows *out, const int32_t *sel,

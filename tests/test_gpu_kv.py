@@ -704,6 +704,53 @@ def test_attend_selected_lists():
     K.check_attention(c, out, lse, K.attention(c, 0.125, sel=kept), "lists")
 
 
+def test_attend_selected_page_named_twice():
+    """A list that names a page again behind a smaller entry counts its keys twice."""
+    c = K.Case([(1, 128)], dtype=F16, d=32, h=1, group=2, page=16)
+    sel = torch.tensor([[[5, -1, 5, 2, 7, 6]]], dtype=torch.int32)  # kept: 5, 5, 7
+    log("page named twice")
+    out, lse = run_attend(c, 0.2, sel=sel)
+    tok = torch.cat([torch.arange(p * 16, p * 16 + 16) for p in (5, 5, 7)])
+    rows = c.table[0].long()[tok // 16] * 16 + tok % 16
+    k64, v64 = (x.double().view(-1, 1, 32)[rows, 0] for x in (c.k, c.v))
+    s = (k64 @ c.q[0].double().t() * 0.2).t()
+    z = torch.logsumexp(s, 1)
+    want = torch.exp(s - z[:, None]) @ v64
+    # as K.attention: scores, weights, sums of 48 terms, the output
+    delta = float((c.q[0].double().abs() @ k64.abs().t()).max()) * 0.2 * 40 * K.U32 + 8 * K.U32
+    u = K.half_step(F16)
+    tol = u * want.abs() + (u + 2 * delta + 56 * K.U32) * (torch.exp(s - z[:, None]) @ v64.abs()) + 2.0 ** -25
+    assert ((out[0].cpu().double() - want).abs() <= tol).all()
+    assert ((lse[0].cpu().double() - z).abs() <= delta + 60 * K.U32 * (1 + z.abs())).all()
+
+
+def test_batch_in_two_calls():
+    """The sequences up to s and from s on, over the same rows: each call leaves the other's rows as
+    they were, and together they give what one call gives."""
+    c = K.Case([(40, 200), (30, 90), (1, 700), (1, 33), (0, 5), (1, 260)], dtype=BF16, h=4, group=2, d=64,
+               page=16, fill=math.nan, tail_rows=2)
+    k, v = c.pools()
+    cache, q = kv.Cache(k, v), c.wide_q.cuda()[:, :8]
+    start, kv_len, table = c.q_start.cuda(), c.kv_len.cuda(), c.table.cuda()
+    ref = K.attention(c, 0.125)
+    sel_ref = K.select(c, K.all_bounds(c), 1, 1, 4)
+    out, lse = torch.full_like(c.q, PAD).cuda(), torch.full((c.n, 8), PAD, device="cuda")
+    sel = torch.full((c.n, 4, 4), -7, dtype=torch.int32, device="cuda")
+    log("two calls")
+    for a, b, max_q, max_kv in ((2, 6, 1, 700), (0, 2, 40, 200)):
+        part = kv.Batch(start[a:b + 1], kv_len[a:b], table[a:b], max_q, max_kv)
+        kv.attend(cache, part, q, out, 0.125, lse=lse,
+                  workspace=ws(kv.attend_workspace(cache, part, c.n, 8)))
+        kv.select(cache, part, K.all_bounds(c).cuda(), q, sel,
+                  workspace=ws(kv.select_workspace(cache, part, c.n, 4)))
+        torch.cuda.synchronize()
+        if a:
+            assert (out[:70] == PAD).all() and (lse[:70] == PAD).all() and (sel[:70] == -7).all()
+    K.check_attention(c, out, lse, ref, "two calls")
+    assert torch.equal(sel.cpu(), sel_ref)
+    assert (out[-2:] == PAD).all() and (lse[-2:] == PAD).all()
+
+
 # ---------------------------------------------------------------- together
 
 def test_decode_loop_with_the_compressed_store():
