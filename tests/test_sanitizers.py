@@ -65,3 +65,35 @@ def test_abi_host_code_under_asan_ubsan(tmp_path):
     r = _run([exe, "no-device"], env=ENV, timeout=120)
     assert "abi sanitizer run ok" in r.stdout
     assert "ERROR: AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr
+
+
+def test_kv_host_code_under_asan_ubsan(tmp_path):
+    """The paged K/V calls' argument checks (api_kv.hip), driven by tests/helpers/kv_sanitize_main.c with
+    every field at the ends of its range."""
+    import torch
+    if torch.cuda.device_count() > 0:
+        pytest.skip("the no-device calls need a machine without a GPU")
+    csrc = os.path.join(ROOT, "host_transfer_amd", "csrc")
+    build = os.path.join(ROOT, "host_transfer_amd", "_build")
+    objs = [os.path.join(build, f + ".hip.o")
+            for f in ("compress", "gather", "gather_cache", "meta", "probe", "kv_append", "kv_attend",
+                      "kv_chunk", "kv_decode", "kv_select")]
+    if not all(os.path.exists(o) for o in objs):
+        from host_transfer_amd.csrc import build as hb
+        hb.build()
+    san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+           "-Xarch_host", "-fno-omit-frame-pointer"]
+    for f in ("api", "api_kv"):
+        objs.append(str(tmp_path / (f + "_san.o")))
+        _run([HIPCC, "--offload-arch=gfx950", "-O1", "-g", "-std=c++17", "-fPIC", "-Xclang",
+              "-target-feature", "-Xclang", "-packed-fp32-ops"] + san +
+             ["-I", os.path.join(ROOT, "include"), "-I", csrc, "-c", os.path.join(csrc, f + ".hip"), "-o",
+              objs[-1]])
+    objs.append(str(tmp_path / "kv_main.o"))
+    _run([HIPCC, "-x", "c", "-O1", "-g"] + san + ["-I", os.path.join(ROOT, "include"), "-c",
+         os.path.join(ROOT, "tests", "helpers", "kv_sanitize_main.c"), "-o", objs[-1]])
+    exe = str(tmp_path / "kv_san")
+    _run([HIPCC, "--offload-arch=gfx950"] + san[:4] + ["-o", exe] + objs)
+    r = _run([exe], env=ENV, timeout=120)
+    assert "kv sanitizer run ok" in r.stdout and "status" not in r.stdout, r.stdout[-2000:]
+    assert "ERROR: AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr
