@@ -59,12 +59,13 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // banks; V pieces so that the four rows of half a transposed read lie in four 64 B windows.
 //
 // Measured (bf16, 32 query heads on 8 key heads, head_dim 128): one prompt of 16,384 tokens
-// 2.09 ms, 1.05 PFLOP/s, where a library product of 16,384^3 reaches 1.31 on the same card; the
-// matrix cores are busy 52 % of the time, the vector ALU 56 %, at the 1.9 GHz that power
-// leaves.  Without the pipeline (rows through registers, scores, weights and values in turn) it
-// took 2.49 ms.  Ragged chunks of up to 511 rows over 9,001 to 2,701 tokens 250 us, 840 TFLOP/s.
-// No faster: 64 rows a wave, one wave a SIMD (2.09 ms; ragged chunks 380 us where this then took
-// 290), half of the weights beside the values instead of the scores (the same).
+// 2.09 to 2.26 ms from card to card, 0.97 to 1.05 PFLOP/s, where a library product of 16,384^3 reaches
+// 1.31 to 1.37; the matrix cores are busy 52 % of the time, the vector ALU 56 %, at the 1.9 GHz that
+// power leaves.  Without the pipeline (rows through registers, scores, weights and values in turn) it
+// took 2.49 ms where it took 2.13 with it.  Ragged chunks of up to 511 rows over 9,001 to 2,701 tokens
+// 243 us, 870 TFLOP/s; one prompt of 2,048 tokens 57 us, 600 TFLOP/s (too few tiles for all CUs).
+// No faster: 64 rows a wave, one wave a SIMD (2.09 ms on a card where this took the same; ragged chunks
+// 380 us where this then took 290), half of the weights beside the values instead of the scores (the same).
 template <typename T, int DP, bool kExact>  // kExact: head_dim == DP == the LDS row
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     Cache cache, Batch b, Rows q, Rows out, float scale, uint32_t window, bool causal,

@@ -30,8 +30,8 @@ constexpr int kWaves = 4;
 // 32 B: the eight rows that half a wave reads then lie in eight different 32 B
 // windows of the banks for every head_dim that is a multiple of 32.
 //
-// Measured (with the join): 20 sequences of up to 2,048 tokens, 40 heads (814 MB) 157 us, 5.2 TB/s;
-// 4 sequences of up to 131,072 tokens, 32 query heads on 8 key heads (1.61 GB) 291 us, 5.5 TB/s, as
+// Measured (with the join): 20 sequences of up to 2,048 tokens, 40 heads (814 MB) 158 us, 5.2 TB/s;
+// 4 sequences of up to 131,072 tokens, 32 query heads on 8 key heads (1.61 GB) 292 us, 5.5 TB/s, as
 // a large copy runs; 8 rows' lists of 2,048 tokens (67 MB) 22 us.  Lists come from L2 more than from HBM
 // and want three waves a SIMD (280 rows' lists 133 us in all with three, 155 with two, 172
 // with four, which spill); whole contexts two (131,072 tokens 291 us, 300 with three).  Loads of the next
