@@ -256,7 +256,7 @@ __global__ __launch_bounds__(256, kSelected && DP <= 128 ? 3 : 1) void k_kv_deco
     V8<T> p;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-// (the product rounded as the base was: huge scores, too, stay at most kLift above it)
+// (the product rounded as the base was: the largest of huge scores, too, is the base itself)
 #pragma clang fp contract(off)
       const float y = exp2_raw(x[e] - base);
       z += y;
