@@ -196,8 +196,9 @@ int ibp_kv_attend_workspace(const ibp_kv_cache *cache, const ibp_kv_batch *batch
  *   workspace ibp_kv_select_workspace() bytes, 16 B aligned: for each row and key
  *             head about 12 for each of the ceil(max_kv / page_tokens) pages, rounded up
  *             to 256 pages (none where n_select covers them all).  8,192 rows of 8
- *             heads over 4,096 pages take 3.2 GB: a long prompt's rows are
- *             best given some at a time, with the same sel and workspace.
+ *             heads over 4,096 pages take 3.2 GB: a long prompt's rows are best
+ *             given some at a time (q and sel from that row on, n_rows and q_start
+ *             of them alone, kv_len up to the last of them), one workspace for all.
  */
 int ibp_kv_select(const ibp_kv_cache *cache, const ibp_kv_batch *batch, const void *bounds,
                   uint64_t n_bounds, const ibp_kv_rows *q, uint32_t n_first, uint32_t n_last,

@@ -751,6 +751,61 @@ def test_batch_in_two_calls():
     assert (out[-2:] == PAD).all() and (lse[-2:] == PAD).all()
 
 
+def test_select_rows_some_at_a_time():
+    """A prompt's rows in pieces, each with the kv_len that its last row has: the whole call's lists,
+    from a smaller workspace."""
+    c = K.Case([(90, 700)], dtype=BF16, h=2, group=2, d=64, page=8, tail_rows=0)
+    bounds = K.all_bounds(c).cuda()
+    cache, q, table = kv.Cache(*c.pools()), c.wide_q.cuda()[:, :4], c.table.cuda()
+    sel = torch.full((90, 2, 6), -7, dtype=torch.int32, device="cuda")
+    log("rows some at a time")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    whole = kv.select_workspace(cache, gpu_batch(c), 90, 6)
+    for a, b in ((0, 40), (40, 41), (41, 90)):
+        part = kv.Batch(i32(0, b - a), i32(700 - 90 + b), table, b - a, 700)
+        need = kv.select_workspace(cache, part, b - a, 6)
+        assert need < whole
+        kv.select(cache, part, bounds, q[a:b], sel[a:b], workspace=ws(need))
+    torch.cuda.synchronize()
+    assert torch.equal(sel.cpu(), K.select(c, bounds.cpu(), 1, 1, 6))
+
+
+@pytest.mark.parametrize("q_len,h", [(1, 1), (2, 4), (40, 1), (70, 4)])
+def test_attend_infinite_scores(q_len, h):
+    """A score of +inf makes its row NaN, its log of the sum too, whatever split it lies in; a score of
+    -inf is a weight of zero, and rows that do not see the key are as without it."""
+    n, page = 600, 16
+    for max_kv in (None, 5000, 60000):
+        c = K.Case([(q_len, n), (q_len, 333)], dtype=BF16, d=64, h=h, group=2, page=page, seed=7)
+        plain = K.Case([(q_len, n), (q_len, 333)], dtype=BF16, d=64, h=h, group=2, page=page, seed=7)
+        for x in (c, plain):
+            if max_kv:
+                wider_table(x, max_kv)
+        c.q[..., 0] = torch.where(torch.arange(2 * h) % 2 == 0, 1.0, -1.0).to(BF16)
+        plain.q[..., 0] = c.q[..., 0]
+        j = 333 - 1 - q_len // 2  # of the second sequence: seen by its later rows
+        at = (int(c.table[1, j // page]), j % page)
+        c.k[at][:, 0] = math.inf
+        log(f"infinite scores q={q_len} h={h} max_kv={max_kv}")
+        out, lse = run_attend(c, 0.125, max_kv=max_kv)
+        want = list(K.attention(plain, 0.125))
+        # where the score is -inf the key counts as one that is not there
+        gone = K.Case([(q_len, n), (q_len, 333)], dtype=BF16, d=64, h=h, group=2, page=page, seed=7)
+        gone.q, gone.table, keys = c.q, c.table, gone.keys
+
+        def without(s, upto=None):
+            pos, rows = keys(s, upto)
+            return (pos[pos != j], rows[pos != j]) if s == 1 else (pos, rows)
+        gone.keys = without
+        left = K.attention(gone, 0.125)
+        for r, s, pos in c.rows():
+            if s == 1 and pos >= j:
+                for t in range(4):
+                    want[t][r, 1::2] = left[t][r, 1::2]
+                want[0][r, 0::2], want[1][r, 0::2] = math.nan, math.nan
+        K.check_attention(c, out, lse, want, f"infinite scores, max_kv={max_kv}")
+
+
 # ---------------------------------------------------------------- together
 
 def test_decode_loop_with_the_compressed_store():
