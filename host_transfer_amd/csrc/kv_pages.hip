@@ -18,6 +18,12 @@ struct Share {
   int32_t held, last, keep;
 };
 
+// Many pages that a request gives back: entries wanted .. wanted + n - 1.
+struct Gift {
+  uint32_t tid;
+  int32_t wanted, n;
+};
+
 // Exclusive prefix sums over the workgroup's threads; the sums of all in `all`.
 template <int N>
 __device__ __forceinline__ void scan(uint64_t (&v)[N], uint64_t (&all)[N], uint64_t (*s)[N]) {
@@ -100,7 +106,10 @@ __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step
   __shared__ unsigned long long s_taken;
   __shared__ Share s_share[kOne ? kThreads : 1];
   __shared__ int32_t s_start[kOne ? kThreads + 1 : 1];
-  const uint32_t tid = threadIdx.x, lane = tid % kWave;
+  __shared__ Gift s_gift[kThreads];
+  __shared__ uint64_t s_at[kThreads];
+  __shared__ unsigned int s_ended;
+  const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const uint32_t turns = (step.n_seqs + kThreads - 1) / kThreads;
   if (tid == 0) {
     s_unserved = 0;
@@ -130,55 +139,81 @@ __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step
     held = min(held, (int32_t)pool.max_pages);
     fits = fits && wanted <= (int32_t)pool.max_pages;
   };
-  // pages that the request gives back; its entries from `wanted` on, a few by each thread itself, more
-  // by its wave
-  constexpr int32_t kFew = 8;
+  // Pages that the request gives back, its entries from `wanted` on: up to kFew by its own thread, more
+  // by the workgroup's waves in turn, kAtOnce entries in flight (`ended` lists those requests; five
+  // of 500 pages one after another in their wave, 64 entries at a time, made a step of 250 requests take
+  // 20 us where it takes 12).
+  constexpr int32_t kFew = 4, kAtOnce = 4 * kWave;
+  auto few = [&](uint32_t t, int32_t (&ids)[kFew], int32_t n) {
+    const int32_t* row = pool.table + (uint64_t)(t * kThreads + tid) * pool.table_stride + wanted;
+#pragma unroll
+    for (int32_t j = 0; j < kFew; ++j) ids[j] = row[min(j, n - 1)];
+  };
   auto gives = [&](uint32_t t) -> uint64_t {
-    const uint32_t s = t * kThreads + tid;
     const int32_t n = fits ? max(held - wanted, 0) : 0;
     uint64_t some = 0;
-    if (n > 0) {
-      const int32_t* row = pool.table + (uint64_t)s * pool.table_stride + wanted;
+    if (tid == 0) s_ended = 0;
+    __syncthreads();
+    if (n > kFew) {
+      s_gift[atomicAdd(&s_ended, 1u)] = Gift{tid, wanted, n};
+    } else if (n > 0) {
+      int32_t ids[kFew];
+      few(t, ids, n);
 #pragma unroll
-      for (int32_t j = 0; j < kFew; ++j) some += j < n && is_page(pool, row[min(j, n - 1)]);
+      for (int32_t j = 0; j < kFew; ++j) some += j < n && is_page(pool, ids[j]);
     }
-    for (uint64_t more = __ballot(n > kFew); more; more &= more - 1) {
-      const int l = __builtin_ctzll(more);
-      const int32_t nl = __shfl(n, l);
-      const int32_t* row = pool.table + (uint64_t)(s - lane + l) * pool.table_stride + __shfl(wanted, l);
+    __syncthreads();
+    for (uint32_t e = wave; e < s_ended; e += kWaves) {
+      const Gift g = s_gift[e];
+      const int32_t* row = pool.table + (uint64_t)(t * kThreads + g.tid) * pool.table_stride + g.wanted;
       uint32_t c = 0;
-      for (int32_t j = kFew + (int32_t)lane; j < nl; j += kWave) c += is_page(pool, row[j]);
+      for (int32_t j = (int32_t)lane; j < g.n; j += kAtOnce) {
+        int32_t ids[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) ids[a] = j + a * kWave < g.n ? row[j + a * kWave] : -1;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) c += is_page(pool, ids[a]);
+      }
 #pragma unroll
       for (int d = 1; d < kWave; d <<= 1) c += __shfl_xor(c, d);
-      if ((int)lane == l) some += c;
+      if (lane == 0) s_at[g.tid] = c;
     }
-    return some;
+    __syncthreads();
+    return n > kFew ? s_at[tid] : some;
   };
   // the same entries to the stack, from place `at` on
   auto give = [&](uint32_t t, uint64_t at) {
-    const uint32_t s = t * kThreads + tid;
     const int32_t n = fits ? max(held - wanted, 0) : 0;
-    if (n > 0) {
-      const int32_t* row = pool.table + (uint64_t)s * pool.table_stride + wanted;
-      for (int32_t j = 0; j < min(n, kFew); ++j) {
-        const int32_t id = row[j];
-        if (is_page(pool, id)) {
-          if (at < pool.n_pages) pool.free_pages[at] = id;
+    if (n > kFew) s_at[tid] = at;
+    __syncthreads();
+    if (n > 0 && n <= kFew) {
+      int32_t ids[kFew];
+      few(t, ids, n);
+#pragma unroll
+      for (int32_t j = 0; j < kFew; ++j)
+        if (j < n && is_page(pool, ids[j])) {
+          if (at < pool.n_pages) pool.free_pages[at] = ids[j];
           ++at;
         }
-      }
     }
-    for (uint64_t more = __ballot(n > kFew); more; more &= more - 1) {
-      const int l = __builtin_ctzll(more);
-      const int32_t nl = __shfl(n, l);
-      const int32_t* row = pool.table + (uint64_t)(s - lane + l) * pool.table_stride + __shfl(wanted, l);
-      uint64_t to = __shfl(at, l);
-      for (int32_t j = kFew; j < nl; j += kWave) {
-        const int32_t id = j + (int32_t)lane < nl ? row[j + lane] : -1;
-        const uint64_t there = __ballot(is_page(pool, id));
-        const uint64_t mine = to + __builtin_popcountll(there & ((1ull << lane) - 1));
-        if (is_page(pool, id) && mine < pool.n_pages) pool.free_pages[mine] = id;
-        to += __builtin_popcountll(there);
+    for (uint32_t e = wave; e < s_ended; e += kWaves) {
+      const Gift g = s_gift[e];
+      const int32_t* row = pool.table + (uint64_t)(t * kThreads + g.tid) * pool.table_stride + g.wanted;
+      uint64_t to = s_at[g.tid];
+      for (int32_t j = 0; j < g.n; j += kAtOnce) {
+        int32_t ids[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const int32_t k = j + a * kWave + (int32_t)lane;
+          ids[a] = k < g.n ? row[k] : -1;
+        }
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const uint64_t there = __ballot(is_page(pool, ids[a]));
+          const uint64_t mine = to + __builtin_popcountll(there & ((1ull << lane) - 1));
+          if (is_page(pool, ids[a]) && mine < pool.n_pages) pool.free_pages[mine] = ids[a];
+          to += __builtin_popcountll(there);
+        }
       }
     }
   };
