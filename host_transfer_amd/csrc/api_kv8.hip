@@ -129,4 +129,58 @@ int ibp_kv8_append(const ibp_kv8_cache* cache, const ibp_kv_batch* batch, uint32
   return ibp::clear_error();
 }
 
+int ibp_kv8_attend(const ibp_kv8_cache* cache, const ibp_kv_batch* batch, uint32_t dtype,
+                   const ibp_kv_rows* q, const ibp_kv_rows* out, float scale, uint32_t window,
+                   unsigned flags, float* lse, void* workspace, uint64_t workspace_bytes,
+                   void* stream) {
+  const char* name = "ibp_kv8_attend";
+  ibp::kv::Cache8 c;
+  ibp::kv::Batch b;
+  ibp::kv::Rows qr, orow;
+  int r;
+  if (flags & ~IBP_KV_CAUSAL) return set_error(IBP_ERR_FLAGS, "%s: unknown flags 0x%x", name, flags);
+  if (window && !(flags & IBP_KV_CAUSAL))
+    return set_error(IBP_ERR_FLAGS, "%s: a window needs IBP_KV_CAUSAL", name);
+  if ((r = check_cache8(name, cache, true, &c)) || (r = check_dtype(name, dtype)) ||
+      (r = check_batch(name, batch, paging(c), true, true, &b)) ||
+      (r = check_rows(name, "q", q, b.n_rows, c.head_dim, false, &qr)) ||
+      (r = check_rows(name, "out", out, b.n_rows, c.head_dim, true, &orow)) ||
+      (r = check_group(name, paging(c), qr.n_heads)) || (r = check_items(name, b.n_rows, qr.n_heads)))
+    return r;
+  if (orow.n_heads != qr.n_heads)
+    return set_error(IBP_ERR_SIZE, "%s: out has %u heads, q has %u", name, orow.n_heads, qr.n_heads);
+  if (b.n_rows && (orow.p == qr.p || (same_strides(orow, qr) && rows_overlap(orow, qr, b.n_rows, c.head_dim))))
+    return set_error(IBP_ERR_SIZE, "%s: out must not overlap q", name);
+  if (!(fabsf(scale) <= 0x1p125f))  // (scores are in the exponent of 2, of fp16 rows of halves: times 2.89)
+    return set_error(IBP_ERR_SIZE, "%s: scale must be finite, its magnitude at most 2^125", name);
+  if (lse && !aligned(lse, 4)) return set_error(IBP_ERR_ALIGN, "%s: misaligned lse", name);
+  if ((r = require_device(name))) return r;
+  uint64_t need = 0;
+  hipError_t e = ibp::kv::attend8_workspace(c, b, qr.n_heads, &need);
+  if (e != hipSuccess) return hip_fail(e, name);
+  if ((r = check_workspace(name, workspace, workspace_bytes, need))) return r;
+  if (b.n_rows == 0 || b.n_seqs == 0 || b.max_q == 0) return ibp::clear_error();
+  e = ibp::kv::launch_attend8(c, dtype, b, qr, orow, scale, window > 0x7FFFFFFFu ? 0 : window,
+                              (flags & IBP_KV_CAUSAL) != 0, lse, workspace, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, name);
+  return ibp::clear_error();
+}
+
+int ibp_kv8_attend_workspace(const ibp_kv8_cache* cache, const ibp_kv_batch* batch,
+                             uint32_t n_q_heads, uint64_t* bytes) {
+  const char* name = "ibp_kv8_attend_workspace";
+  if (!bytes) return set_error(IBP_ERR_NULL, "%s: bytes is required", name);
+  ibp::kv::Cache8 c;
+  ibp::kv::Batch b;
+  int r;
+  if ((r = check_cache8(name, cache, false, &c)) ||
+      (r = check_batch(name, batch, paging(c), false, true, &b)) ||
+      (r = check_group(name, paging(c), n_q_heads)) || (r = check_items(name, b.n_rows, n_q_heads)) ||
+      (r = require_device(name)))
+    return r;
+  hipError_t e = ibp::kv::attend8_workspace(c, b, n_q_heads, bytes);
+  if (e != hipSuccess) return hip_fail(e, name);
+  return ibp::clear_error();
+}
+
 }  // extern "C"

@@ -5,8 +5,6 @@
 namespace ibp {
 namespace kv {
 
-namespace {
-
 // How a call is run.
 //   few    Up to 16 rows share a sequence's keys (one new token, or a few, with its group of
 //          heads), or each row has its own list of pages.
@@ -59,8 +57,6 @@ uint64_t partial_bytes(const Cache& c, const Batch& b, uint32_t n_q_heads, const
   if (p.splits == 1) return 0;
   return (uint64_t)b.n_rows * n_q_heads * p.splits * (c.head_dim + 2) * 4;
 }
-
-}  // namespace
 
 hipError_t attend_workspace(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
                             uint64_t* bytes) {

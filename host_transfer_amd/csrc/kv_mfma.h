@@ -224,6 +224,11 @@ struct AttendPlan {
   uint64_t blocks;
 };
 
+// kv_attend.hip
+hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
+                     uint32_t window, AttendPlan* p);
+uint64_t partial_bytes(const Cache& c, const Batch& b, uint32_t n_q_heads, const AttendPlan& p);
+
 hipError_t launch_decode(const AttendPlan& p, const Cache& c, uint32_t dtype, const Batch& b,
                          const Rows& q, const Rows& out, const int32_t* sel, uint32_t n_select,
                          float scale, uint32_t window, bool causal, float* lse, Partial part,

@@ -33,6 +33,8 @@ _pc, _pr, _pb = (ctypes.POINTER(x) for x in (_CCache8, _CRows, _CBatch))
 # name -> argument types (all return int status)
 _SIGS = {
     "ibp_kv8_append": [_pc, _pb, _u32, _pr, _pr, _pr, _pr, _vp, _vp, _u64, _u32, _vp, _vp, _f, _u, _vp],
+    "ibp_kv8_attend": [_pc, _pb, _u32, _pr, _pr, _f, _u32, _u, _vp, _vp, _u64, _vp],
+    "ibp_kv8_attend_workspace": [_pc, _pb, _u32, ctypes.POINTER(_u64)],
 }
 for _name, _args in _SIGS.items():
     _fn = getattr(ibp._lib, _name)
@@ -131,3 +133,25 @@ def append(cache, batch, k, v, q=None, q_out=None, positions=None, rope=None, fl
         _plain("rope", rope, torch.float32, 0, dev), n_positions or 0, rope_dim or 0,
         _of_dtype("q_norm", of, q_norm, cache.head_dim, dev),
         _of_dtype("k_norm", of, k_norm, cache.head_dim, dev), eps, flags, _stream(stream, dev)))
+
+
+def attend_workspace(cache, batch, n_rows, n_q_heads) -> int:
+    """Workspace bytes of attend."""
+    n = _u64()
+    ibp._check(ibp._lib.ibp_kv8_attend_workspace(cache._c, batch._c(cache, n_rows), n_q_heads, n))
+    return n.value
+
+
+def attend(cache, batch, q, out, scale, window=0, flags=CAUSAL, lse=None, workspace=None, n_rows=None,
+           dtype=None, stream=None):
+    """q, out: (rows, heads, head_dim) tensors or Rows (n_rows and dtype are then needed); lse: float32
+    (rows, heads); workspace: a device tensor of at least attend_workspace() bytes."""
+    dev = _current(cache, batch)
+    c_dtype, dtype = _dtype("q", q, dtype)
+    of = _Of(cache, dtype)
+    qr, n = _rows("q", of, q, n_rows, dev)
+    orow, _ = _rows("out", of, out, n, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    ibp._check(ibp._lib.ibp_kv8_attend(
+        cache._c, batch._c(cache, n), c_dtype, qr, orow, scale, window, flags,
+        _plain("lse", lse, torch.float32, n * qr.n_heads, dev), ws, ws_bytes, _stream(stream, dev)))

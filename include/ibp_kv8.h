@@ -70,9 +70,10 @@ int ibp_kv8_append(const ibp_kv8_cache *cache, const ibp_kv_batch *batch, uint32
 
 /*
  * ibp_kv8_attend -- ibp_kv_attend over a cache in 8 bits: the same rows, masks, outputs, log of the
- * sums and refusals, with K and V the values that the codes and exponents stand for (they are
- * exact in the rows' type, but in IBP_KV_F16 below 2^-20, where they are rounded to multiples of
- * 2^-23).
+ * sums and refusals (but scale at most 2^125), with K and V the values that the codes and exponents
+ * stand for.  They are exact in the rows' type, but in IBP_KV_F16 below 2^-20, where they are
+ * rounded to multiples of 2^-23, and in IBP_KV_BF16 values of V below 2^-94 and of K below 2^-126,
+ * which may be taken as zero.
  *   workspace   ibp_kv8_attend_workspace() bytes, 16 B aligned (NULL if 0).
  */
 int ibp_kv8_attend(const ibp_kv8_cache *cache, const ibp_kv_batch *batch, uint32_t dtype,

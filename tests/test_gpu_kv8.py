@@ -210,3 +210,379 @@ def test_append_long_prompt_beside_single_tokens():
         x = qkv.double()
         check_cache(c, got, K8.append(c, x[:, 3:5], x[:, 5:], placed), 0.0)
         check_q(c, got[4], x[:, :3], placed, held, False, False)
+
+
+# ---------------------------------------------------------------- attention
+
+def run_attend(c, scale, causal=True, window=0, max_q=None, max_kv=None):
+    cache, batch = kv8.Cache(*c.pools8()), gpu_batch(c, max_q, max_kv)
+    hq = c.h * c.group
+    q = c.wide_q.cuda()[:, :hq]
+    out = torch.full((c.n, hq + 1, c.d), PAD, dtype=c.dtype, device="cuda")
+    lse = torch.full((c.n, hq), PAD, device="cuda")
+    w = ws(kv8.attend_workspace(cache, batch, c.n, hq))
+    kv8.attend(cache, batch, q, out[:, :hq], scale, window=window, flags=kv8.CAUSAL if causal else 0, lse=lse,
+               workspace=w)
+    torch.cuda.synchronize()
+    assert (out[:, hq] == PAD).all(), "wrote past the heads of out"
+    return out[:, :hq], lse
+
+
+def n_splits(c, max_kv=None):
+    """Into how many parts a call splits each row's keys: its workspace has head_dim + 2 floats of each."""
+    hq = c.h * c.group
+    need = kv8.attend_workspace(kv8.Cache(*c.pools8()), gpu_batch(c, max_kv=max_kv), c.n, hq)
+    return need // (c.n * hq * (c.d + 2) * 4)
+
+
+def wider_table(c, max_kv):
+    """The case's page table with room for max_kv tokens; the pages past its own are not there."""
+    room = -(-max_kv // c.page)
+    if c.table.shape[1] < room:
+        more = torch.full((c.table.shape[0], room - c.table.shape[1]), -1, dtype=torch.int32)
+        c.table = torch.cat([c.table, more], 1)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("q_len", [1, 20])
+def test_values_are_exact(dtype, q_len):
+    """Every code with exponents over the type's range: a row that sees one key gives its value itself."""
+    d, h = 256, 4
+    exps = list(range(103, 136)) if dtype is F16 else list(range(1, 247, 3)) + [0, 246]
+    c = K8.Case8([(q_len, 1)] * len(exps), dtype=dtype, h=h, group=1, d=d, page=16, block=4, extra=3)
+    bits = torch.arange(256, dtype=torch.int64)
+    for i, e in enumerate(exps):
+        for hh in range(h):
+            c.v8.view(torch.uint8)[int(c.table[i, 0]), 0, hh] = ((bits * (2 * hh + 1)) % 256).to(torch.uint8)
+            c.ve[int(c.table[i, 0]), 0, hh] = e
+    c.renew()
+    log(f"exact values {dtype} q={q_len}")
+    out, _ = run_attend(c, 0.1, causal=False)
+    # (bf16: a weight of 2^-32 times a value below 2^-94 is below fp32's normal numbers)
+    most, least = (65504.0, 2.0 ** -20) if dtype is F16 else (3.4e38, 2.0 ** -94)
+    for i in range(len(exps)):
+        want = c.v[int(c.table[i, 0]), 0].clamp(-most, most)
+        for r in range(q_len):
+            got = out[i * q_len + r].cpu().double()
+            same = (got == want) | (torch.isnan(got) & torch.isnan(want))
+            small = want.abs() < least
+            assert same[~small].all(), (exps[i], got[~same & ~small][:5], want[~same & ~small][:5])
+            step = 2.0 ** -24 if dtype is F16 else least
+            assert ((got - want).abs()[small] <= step).all()
+
+
+ATTEND_LENS = [(1, 1), (3, 3), (0, 0), (17, 64), (1, 65), (2, 200), (0, 31), (130, 300), (66, 66)]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,h,group,page,block", [
+    (16, 1, 1, 16, 16), (48, 2, 3, 8, 8), (64, 2, 4, 16, 16), (80, 1, 2, 24, 8), (96, 2, 1, 1, 1), (128, 2, 8, 16, 16),
+    (128, 1, 5, 64, 32), (144, 1, 2, 16, 4), (192, 2, 2, 32, 32), (256, 1, 20, 16, 16)])
+def test_attend(dtype, d, h, group, page, block):
+    c = K8.Case8(ATTEND_LENS, dtype=dtype, h=h, group=group, d=d, page=page, block=block, strange=True,
+                 fill=math.nan, tail_rows=3, head_major=page == 16)
+    scale = 1 / math.sqrt(d)
+    for causal, window in ((True, 0), (True, 1), (True, 50), (False, 0)):
+        log(f"attend {dtype} d={d} h={h} group={group} page={page} block={block} causal={causal} window={window}")
+        out, lse = run_attend(c, scale, causal, window)
+        K.check_attention(c, out, lse, K.attention(c, scale, causal=causal, window=window),
+                          f"causal={causal} window={window}")
+        assert (out[c.n - 3:] == PAD).all() and (lse[c.n - 3:] == PAD).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("d,h,group,page,block", [
+    (64, 2, 1, 16, 16), (80, 1, 4, 24, 24), (96, 4, 2, 16, 8), (128, 2, 4, 16, 16), (128, 1, 16, 1, 1),
+    (128, 4, 8, 64, 16), (192, 1, 17, 64, 64), (256, 1, 3, 32, 16), (256, 4, 2, 16, 16)])
+def test_attend_single_tokens(dtype, d, h, group, page, block):
+    """One new token a sequence, from one key to several splits of the keys."""
+    lens = [(1, n) for n in (1, 2, 15, 16, 17, 31, 64, 65, 127, 257, 1000, 2049)] + [(0, 0), (1, 700)]
+    c = K8.Case8(lens, dtype=dtype, h=h, group=group, d=d, page=page, block=block, strange=True, fill=math.nan,
+                 tail_rows=1)
+    scale = 0.7 / math.sqrt(d)
+    for causal, window, max_kv in ((True, 0, None), (True, 33, None), (False, 0, None), (True, 0, 20000)):
+        if max_kv:
+            wider_table(c, max_kv)
+        log(f"single tokens {dtype} d={d} group={group} page={page} window={window} max_kv={max_kv}")
+        out, lse = run_attend(c, scale, causal, window, max_kv=max_kv)
+        K.check_attention(c, out, lse, K.attention(c, scale, causal=causal, window=window),
+                          f"window={window} max_kv={max_kv}")
+        assert (out[c.n - 1:] == PAD).all() and (lse[c.n - 1:] == PAD).all()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("q_len,d,h,group,page", [
+    (2, 128, 2, 8, 16), (3, 64, 4, 8, 16), (5, 128, 8, 4, 16), (4, 96, 1, 8, 24), (9, 192, 4, 3, 16), (6, 256, 1, 5, 64),
+    (17, 128, 4, 1, 16), (32, 64, 1, 1, 16), (33, 128, 2, 1, 16), (11, 128, 4, 3, 32)])
+def test_attend_drafted_tokens(dtype, q_len, d, h, group, page):
+    """Some new tokens of each sequence, around the sizes at which another way of running them begins;
+    unsplit and in splits."""
+    lens = [(q_len, n) for n in (q_len, q_len + 1, 64, 65, 200, 700, 1300)] + [(0, 9), (1, 500), (max(1, q_len - 1), 90)]
+    c = K8.Case8(lens, dtype=dtype, h=h, group=group, d=d, page=page, block=page // 2, strange=True, fill=math.nan,
+                 tail_rows=2)
+    c.table[4, 3 % c.table.shape[1]] = -1
+    wider_table(c, 20000)
+    scale = 1 / math.sqrt(d)
+    for causal, window, max_kv in ((True, 0, None), (True, 70, None), (False, 0, None), (True, 0, 20000)):
+        log(f"drafts {dtype} q={q_len} d={d} h={h} group={group} causal={causal} window={window} max_kv={max_kv}")
+        out, lse = run_attend(c, scale, causal, window, max_kv=max_kv)
+        K.check_attention(c, out, lse, K.attention(c, scale, causal=causal, window=window),
+                          f"causal={causal} window={window} max_kv={max_kv}")
+        assert (out[c.n - 2:] == PAD).all() and (lse[c.n - 2:] == PAD).all()
+
+
+@pytest.mark.parametrize("q", [1, 2, 5, 40, 200])
+def test_attend_bad_pages_and_lengths(q):
+    """Pages that are not there (ids of every wrong kind), lengths past the bounds given, rows
+    at positions before the first token."""
+    lens = [(q, 400), (q, 170), (q, q - 1 if q < 3 else q // 2), (q, 250)]
+    c = K8.Case8(lens, d=64, h=2, group=2, page=16, fill=math.nan, seed=q)
+    for s, p, bad in ((0, 0, -1), (0, 7, c.n_pages), (0, 24, 1 << 30), (1, 3, -(1 << 31)),
+                      (3, 15, -5), (3, 14, -5), (3, 13, c.n_pages + 7)):
+        c.table[s, p] = bad
+    log(f"bad pages q={q}")
+    out, lse = run_attend(c, 0.125)
+    K.check_attention(c, out, lse, K.attention(c, 0.125), f"q={q}")
+    c.table[0] = -1  # a sequence whose pages are all missing
+    out, lse = run_attend(c, 0.125)
+    K.check_attention(c, out, lse, K.attention(c, 0.125), f"q={q}: no page")
+    # tokens past max_kv are not read, new tokens past max_q are left as they were
+    c = K8.Case8([(q, 400), (q, 170)], d=64, h=2, group=2, page=16, fill=math.nan, seed=q)
+    out, lse = run_attend(c, 0.125, causal=False, max_kv=300)
+    ref = K8.Case8([(q, 400), (q, 170)], d=64, h=2, group=2, page=16, fill=math.nan, seed=q)
+    cut = ref.keys
+    ref.keys = lambda s, upto=None: cut(s, 300)
+    K.check_attention(c, out, lse, K.attention(ref, 0.125, causal=False), f"q={q}: max_kv")
+    if q > 1:
+        out, lse = run_attend(c, 0.125, max_q=q - 1)
+        assert (out[q - 1] == PAD).all() and (out[2 * q - 1] == PAD).all()
+        want = K.attention(c, 0.125)
+        want[4][[q - 1, 2 * q - 1]] = False
+        K.check_attention(c, out, lse, want, f"q={q}: max_q")
+
+
+@pytest.mark.parametrize("q_len,h,group", [(1, 1, 2), (1, 4, 3), (3, 2, 4), (5, 4, 4), (2, 8, 1), (40, 1, 2), (70, 4, 1)])
+def test_attend_nan_in_any_split(q_len, h, group):
+    """NaN values whose weight rounds to zero in 32 bits, in the largest score's split, in others and in
+    masked places; a NaN key: the rows that see them, and no others, carry them, wherever the keys are split."""
+    n, d, page = 1500, 16, 16
+    for max_kv in (None, 9000, 90000):
+        c = K8.Case8([(q_len, n), (q_len, 700)], dtype=BF16, d=d, h=h, group=group, page=page, seed=q_len)
+        if max_kv:
+            wider_table(c, max_kv)
+        c.q[..., 0] = 1.0
+        at = lambda s, j: (int(c.table[s, j // page]), j % page)  # noqa: E731
+        k8, v8 = c.k8.view(torch.uint8), c.v8.view(torch.uint8)
+        k8[..., 0] = 0
+        for s, j in ((0, 777), (1, 3)):  # the largest scores: a code of 448 in a channel of its own
+            k8[at(s, j)][:, 0] = 0x7E
+        for i, j in enumerate((5, 70, 760, 780, 1100, n - 1, n - 2, n - 30, 698)):
+            for s in range(2):
+                if j < c.lens[s][1]:
+                    v8[at(s, j)][:, i + 1] = 0x7F if i % 2 else 0xFF
+        c.renew()
+        splits = n_splits(c, max_kv)
+        log(f"NaN in {splits} splits, q={q_len} h={h} group={group}")
+        assert max_kv is None or splits > (8 if max_kv == 90000 else 1)
+        for causal, window in ((False, 0), (True, 0), (True, 500)):
+            out, lse = run_attend(c, 8.0, causal, window, max_kv=max_kv)
+            K.check_attention(c, out, lse, K.attention(c, 8.0, causal=causal, window=window),
+                              f"{splits} splits, causal={causal} window={window}")
+        k8[at(0, n - 1)][:, 2] = 0x7F
+        c.renew()
+        out, lse = run_attend(c, 1.0, True, 0, max_kv=max_kv)
+        K.check_attention(c, out, lse, K.attention(c, 1.0), f"{splits} splits, a NaN key")
+
+
+@pytest.mark.parametrize("dtype,d,h,group,page", [
+    (BF16, 64, 2, 2, 16), (F16, 128, 1, 4, 24), (BF16, 128, 2, 1, 64), (F16, 96, 1, 2, 16),
+    (BF16, 192, 1, 2, 16), (F16, 256, 1, 2, 32), (BF16, 48, 1, 4, 8)])
+def test_attend_chunks_in_splits(dtype, d, h, group, page):
+    """Chunks whose keys are split over workgroups, into few parts and into many: causal,
+    windowed and open masks, sequences that have no keys in most of the splits, a split whose pages are
+    all missing, rows behind the last sequence left as they were."""
+    c = K8.Case8([(50, 1500), (0, 0), (33, 700), (24, 1100), (1, 64), (60, 60)], dtype=dtype, d=d, h=h,
+                 group=group, page=page, block=page // 2, strange=True, fill=math.nan, tail_rows=2, seed=d + group)
+    c.table[3, 512 // page:-(-768 // page)] = -1
+    c.table[0, 1200 // page] = c.n_pages
+    wider_table(c, 40000)
+    scale = 1 / math.sqrt(d)
+    for causal, window in ((True, 0), (True, 1000), (False, 0)):
+        ref = K.attention(c, scale, causal=causal, window=window)
+        for max_kv, least in ((1500, 2), (4200, 3), (9000, 9), (40000, 40)):
+            splits = n_splits(c, max_kv)
+            log(f"chunks in {splits} splits {dtype} d={d} h={h} group={group} {causal} {window}")
+            assert splits >= least
+            out, lse = run_attend(c, scale, causal, window, max_kv=max_kv)
+            K.check_attention(c, out, lse, ref, f"{splits} splits, causal={causal} window={window}")
+            assert (out[c.n - 2:] == PAD).all() and (lse[c.n - 2:] == PAD).all()
+
+
+@pytest.mark.parametrize("q_len,h", [(1, 1), (2, 4), (40, 2)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attend_ends_of_the_range(dtype, q_len, h):
+    """Values and keys at the upper and lower end of the rows' type, all equal and mixed; scales of both signs and zero."""
+    for e, code in ((135, 0x78), (135, 0x70), (1, 0x7E), (112, 0x01)) if dtype is F16 else \
+            ((246, 0x7E), (245, 0x70), (12, 0x7E), (140, 0x01)):
+        c = K8.Case8([(q_len, 300), (q_len, 77)], dtype=dtype, d=64, h=h, group=2, page=16)
+        c.v8.view(torch.uint8)[:] = code
+        c.ve[:] = e
+        c.ke[:] = 100  # scores near zero: equal weights
+        c.renew()
+        c.v.clamp_(-65504 * 2 if dtype is F16 else -3.4e38, 65504 * 2 if dtype is F16 else 3.4e38)
+        log(f"ends {dtype} q={q_len} h={h} e={e} code={code}")
+        out, lse = run_attend(c, 0.01)
+        ref = list(K.attention(c, 0.01))
+        if dtype is F16:
+            # a mean within the type's range; each value is read as the half of itself, which fp16's
+            # least step, 2^-24, rounds by up to 2^-25: up to 2^-24 of the value, and of a mean of them
+            ref[0], ref[2] = ref[0].clamp(-65504, 65504), ref[2] + 2.0 ** -24
+        K.check_attention(c, out, lse, ref, f"e={e}")
+    for scale in (0.0, -0.3, 5.0):
+        c = K8.Case8([(q_len, 300), (q_len, 77)], dtype=dtype, d=64, h=h, group=2, page=16, strange=True)
+        log(f"scale {scale}")
+        out, lse = run_attend(c, scale)
+        K.check_attention(c, out, lse, K.attention(c, scale), f"scale={scale}")
+
+
+@pytest.mark.parametrize("q_len", [1, 2, 40])
+def test_attend_many_small_weights(q_len):
+    """Thousands of weights far below the largest one: their sum counts, in fp16 too."""
+    n = 6000
+    for dtype in (F16, BF16):
+        c = K8.Case8([(q_len, n)], dtype=dtype, d=64, h=1, group=2, page=16)
+        c.q[:], c.q[..., 0] = 0.0, 1.0
+        c.k8.view(torch.uint8)[:] = 0
+        c.ke[:] = 127
+        c.k8.view(torch.uint8)[int(c.table[0, 3]), 5, 0, 0] = torch.tensor(16.0).to(K8.E4M3).view(torch.uint8)
+        c.renew()
+        log(f"small weights {dtype} q={q_len}")
+        out, lse = run_attend(c, 1.0)
+        K.check_attention(c, out, lse, K.attention(c, 1.0), str(dtype))
+
+
+@pytest.mark.parametrize("n_seqs", [2, 64, 65])
+def test_chunks_of_many_sequences(n_seqs):
+    """Chunks against longer contexts, up to 64 sequences (the longest first) and more."""
+    lens = [(3 + 7 * (s % 5), 60 + 13 * (s * 37 % 50)) for s in range(n_seqs)]
+    lens[0] = (40, 300)
+    c = K8.Case8(lens, dtype=BF16, h=1, group=2, d=64, page=16, fill=math.nan, seed=n_seqs)
+    log(f"chunks of {n_seqs} sequences")
+    out, lse = run_attend(c, 0.125)
+    K.check_attention(c, out, lse, K.attention(c, 0.125), f"{n_seqs}")
+
+
+@pytest.mark.parametrize("q_len", [1, 5, 50])
+def test_pages_beyond_32_bit_offsets(q_len):
+    """A pool of more than 2^32 bytes, its pages used at both ends: append, then attention."""
+    page, h, d = 64, 8, 128
+    n_pages = (1 << 32) // (page * h * d) + 40
+    big = [torch.empty((n_pages, page, h, d), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    exps = [torch.zeros((n_pages, 4, h), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    c = K8.Case8([(q_len, 900), (q_len, 333)], dtype=BF16, d=d, h=h, group=2, page=page, block=16)
+    c.max_rows = c.most_kv = 1 << 30
+    where = torch.arange(c.n_pages)
+    where = torch.where(where % 2 == 0, n_pages - 1 - where, where)  # page of the small pool -> here
+    log(f"far pages q={q_len}")
+    for b, e, codes, ex in zip(big, exps, (c.k8, c.v8), (c.ke, c.ve)):
+        b[where.cuda()] = codes.view(torch.uint8).cuda()
+        e[where.cuda()] = ex.cuda()
+    far = torch.where(c.table >= 0, where[c.table.clamp(min=0).long()].int(), c.table)
+    cache = kv8.Cache(*(x.view(K8.E4M3) for x in big), *exps)
+    batch = kv.Batch(c.q_start.cuda(), c.kv_len.cuda(), far.cuda(), q_len, 900)
+    assert int(far.max()) * page * h * d > 1 << 32
+    rows = torch.randn((c.n, 2 * h, d), generator=torch.Generator().manual_seed(1)).to(BF16)
+    gpu = rows.cuda()
+    kv8.append(cache, batch, gpu[:, :h], gpu[:, h:])
+    placed, _ = placed_rows(c)
+    x = rows.double()
+    ref = K8.append(c, x[:, :h], x[:, h:], placed)
+    got = [b[where.cuda()].cpu().view(K8.E4M3) for b in big] + [e[where.cuda()].cpu() for e in exps]
+    check_cache(c, got, ref, 0.0)
+    c.k8, c.v8, c.ke, c.ve = got
+    c.renew()
+    q = c.wide_q.cuda()[:, :2 * h]
+    out = torch.zeros((c.n, 2 * h, d), dtype=BF16, device="cuda")
+    lse = torch.zeros((c.n, 2 * h), device="cuda")
+    kv8.attend(cache, batch, q, out, 0.1, lse=lse, workspace=ws(kv8.attend_workspace(cache, batch, c.n, 2 * h)))
+    K.check_attention(c, out, lse, K.attention(c, 0.1), "far pages")
+
+
+def test_graph_replay_and_streams():
+    """Append and attention of single tokens, of drafted ones and of chunks in splits captured, replayed
+    with other inputs in the same buffers, eager work between; then attention on two streams at once, each
+    with its workspace.  The same bits as eager calls every time."""
+    for q_len, group, max_kv in ((1, 4, 928), (5, 4, 928), (40, 2, 6000)):
+        c = K8.Case8([(q_len, 900), (q_len, 300), (q_len, 50)], dtype=BF16, d=128, h=2, group=group, page=16)
+        wider_table(c, max_kv)
+        pools = c.pools8()
+        cache, batch, hq = kv8.Cache(*pools), gpu_batch(c, max_kv=max_kv), 2 * group
+        start = [p.clone() for p in pools]
+        q = c.wide_q.cuda()[:, :hq].contiguous()
+        rows = torch.randn((c.n, 4, 128), device="cuda").to(BF16)
+        need = kv8.attend_workspace(cache, batch, c.n, hq)
+        works = [ws(need) for _ in range(3)]
+
+        def reset():
+            for p, s in zip(pools, start):
+                p.view(torch.uint8).copy_(s.view(torch.uint8))
+
+        def step(out, lse, work):
+            kv8.append(cache, batch, rows[:, :2], rows[:, 2:])
+            kv8.attend(cache, batch, q, out, 0.1, lse=lse, workspace=work)
+        got, want = ([torch.zeros_like(q), torch.zeros((c.n, hq), device="cuda")] for _ in range(2))
+        step(*got, works[0])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        log(f"capture q={q_len}")
+        with torch.cuda.graph(graph):
+            step(*got, works[0])
+        for rep in range(4):
+            q.copy_(torch.randn_like(q))
+            rows.copy_(torch.randn_like(rows) * 3 ** rep)
+            batch._keep[1].copy_(torch.tensor([900 - 100 * rep, 300 - 77 * rep, 50 - rep]))
+            reset()
+            step(*want, works[1])
+            torch.cuda.synchronize()
+            after = [p.view(torch.uint8).clone() for p in pools]
+            reset()
+            for t in got:
+                t.fill_(3)
+            works[0].fill_(255)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), rep
+            assert all(torch.equal(p.view(torch.uint8), a) for p, a in zip(pools, after)), rep
+            c.k8, c.v8, c.ke, c.ve = [p.view(torch.uint8).cpu() for p in pools]
+            c.k8, c.v8 = c.k8.view(K8.E4M3), c.v8.view(K8.E4M3)
+            c.renew()
+            c.q, c.lens = q.cpu(), [(q_len, x) for x in batch._keep[1].tolist()]
+            K.check_attention(c, *got, K.attention(c, 0.1), f"replay {rep}")
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        outs = [[torch.zeros_like(q), torch.zeros((c.n, hq), device="cuda")] for _ in range(6)]
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            kv8.attend(cache, batch, q, o[0], 0.1, lse=o[1], workspace=works[1 + i % 2], stream=streams[i % 2])
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+
+
+def test_empty_calls():
+    """No rows, no sequences, a cache whose sequences are all empty."""
+    c = K8.Case8([(0, 0), (0, 40)], d=64, tail_rows=3)
+    pools = c.pools8()
+    before = [p.view(torch.uint8).clone() for p in pools]
+    cache = kv8.Cache(*pools)
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    none = kv.Batch(i32(0), i32(), torch.zeros((0, 4), dtype=torch.int32, device="cuda"), 0, 0)
+    log("empty calls")
+    q = torch.zeros((3, 4, 64), dtype=BF16, device="cuda")
+    out = torch.full_like(q, PAD)
+    for batch in (none, gpu_batch(c), kv.Batch(c.q_start.cuda(), c.kv_len.cuda(), c.table.cuda(), 2, 48)):
+        for n in (0, 3):
+            kv8.append(cache, batch, q[:n, :2], q[:n, 2:], q=q[:n], q_out=out[:n])
+            kv8.attend(cache, batch, q[:n], out[:n], 1.0, workspace=ws(kv8.attend_workspace(cache, batch, n, 4)))
+    torch.cuda.synchronize()
+    assert (out == PAD).all()
+    assert all(torch.equal(p.view(torch.uint8), b) for p, b in zip(pools, before))
