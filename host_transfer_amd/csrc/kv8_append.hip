@@ -122,12 +122,12 @@ __device__ __forceinline__ float largest(const float (&x)[8], float most) {
 // The waves behind: queries, a wave (several, `parts`, for few rows) per row, as k_kv_append.
 // Bound by reading the 16-bit rows and writing them or half of them.
 template <typename T, int L>
-__global__ __launch_bounds__(256) void k_kv8_append(Cache8 cache, Batch b, Rows k, Rows v, Rows q, Rows q_out,
+__global__ __launch_bounds__(256, 4) void k_kv8_append(Cache8 cache, Batch b, Rows k, Rows v, Rows q, Rows q_out,
                                                     Turning t, const T* __restrict__ q_norm,
                                                     const T* __restrict__ k_norm, uint32_t seq_blocks,
                                                     uint64_t kv_units, uint32_t parts) {
   constexpr uint32_t HW = kWave / L;  // rows of a wave at a time
-  constexpr uint32_t kKeep = 4;
+  constexpr uint32_t kKeep = 2;
   typedef V8<T> v8;
   const uint32_t lane = threadIdx.x % kWave, c = lane % L, sub = lane / L;
   const Pieces p = pieces_of(t, c);
@@ -156,12 +156,7 @@ __global__ __launch_bounds__(256) void k_kv8_append(Cache8 cache, Batch b, Rows 
     const int32_t base = (int32_t)base64, begin = (int32_t)begin64, end = (int32_t)(base64 + B < to ? base64 + B : to);
     const uint32_t page = cache.page.div((uint32_t)base), in = (uint32_t)base - page * cache.page.d;
     const int32_t id = b.table[(uint64_t)(uint32_t)s * b.table_stride + page];
-    if (id < 0 || (uint32_t)id >= cache.n_pages) return;
-    uint8_t* codes = (is_v ? cache.v : cache.k) + (uint64_t)(uint32_t)id * cache.page_stride +
-                     (uint64_t)in * cache.token_stride + (uint64_t)h * cache.head_stride;
-    uint8_t* exp = (is_v ? cache.v_exp : cache.k_exp) +
-                   ((uint64_t)(uint32_t)id * cache.page_blocks + cache.block.div(in)) * cache.n_heads + h;
-    const uint32_t was = begin > base ? valid_exponent(*exp) : 1;
+    const bool there = id >= 0 && (uint32_t)id < cache.n_pages;  // (looked at once the rows are on their way)
     const bool norm = !is_v && k_norm, rotates = !is_v && t.rope;
     v8 w[2] = {};
     if (norm) {
@@ -194,11 +189,6 @@ __global__ __launch_bounds__(256) void k_kv8_append(Cache8 cache, Batch b, Rows 
       }
       return on;
     };
-    auto put = [&](int32_t at, const float (&x)[8], const float (&y)[8], float inv) {
-      uint8_t* dst = codes + (uint64_t)(uint32_t)(at - base) * cache.token_stride;
-      if (p.has0) *(uint2*)(dst + p.c0 * 8) = encode8(x, inv);
-      if (p.has1) *(uint2*)(dst + p.c1 * 8) = encode8(y, inv);
-    };
     float x[kKeep][8], y[kKeep][8], most = 0.f;
     bool on[kKeep];
 #pragma unroll
@@ -206,6 +196,17 @@ __global__ __launch_bounds__(256) void k_kv8_append(Cache8 cache, Batch b, Rows 
       on[i] = row(begin + (int32_t)(i * HW + sub), x[i], y[i]);
       most = largest(y[i], largest(x[i], most));
     }
+    if (!there) return;
+    uint8_t* codes = (is_v ? cache.v : cache.k) + (uint64_t)(uint32_t)id * cache.page_stride +
+                     (uint64_t)in * cache.token_stride + (uint64_t)h * cache.head_stride;
+    uint8_t* exp = (is_v ? cache.v_exp : cache.k_exp) +
+                   ((uint64_t)(uint32_t)id * cache.page_blocks + cache.block.div(in)) * cache.n_heads + h;
+    const uint32_t was = begin > base ? valid_exponent(*exp) : 1;
+    auto put = [&](int32_t at, const float (&x)[8], const float (&y)[8], float inv) {
+      uint8_t* dst = codes + (uint64_t)(uint32_t)(at - base) * cache.token_stride;
+      if (p.has0) *(uint2*)(dst + p.c0 * 8) = encode8(x, inv);
+      if (p.has1) *(uint2*)(dst + p.c1 * 8) = encode8(y, inv);
+    };
     for (int32_t at = begin + (int32_t)(kKeep * HW); at < end; at += HW) {
       float xx[8], yy[8];
       row(at + (int32_t)sub, xx, yy);
@@ -244,20 +245,31 @@ __global__ __launch_bounds__(256) void k_kv8_append(Cache8 cache, Batch b, Rows 
     }
     return;
   }
-  // queries
   u -= kv_units;
   const uint64_t r64 = u / parts;
   if (q.n_heads == 0 || r64 >= b.n_rows) return;
   const uint32_t r = (uint32_t)r64, part = (uint32_t)(u - r64 * parts);
+  const uint32_t per_part = (q.n_heads + parts - 1) / parts;
+  const uint32_t h_begin = part * per_part, h_end = min(h_begin + per_part, q.n_heads);
+  // the next heads' pieces are on their way while these are turned, the first ones during the
+  // chain of loads that says whether the row is placed
+  const T* src = (const T*)q.p + r * q.token_stride;
+  auto heads = [&](uint32_t h, v8& a, v8& d) {
+    a = d = v8{};
+    if (h < h_end && p.has0) a = load_row8(src + (uint64_t)h * q.head_stride + p.c0 * 8);
+    if (h < h_end && p.has1) d = load_row8(src + (uint64_t)h * q.head_stride + p.c1 * 8);
+  };
+  v8 a, d;
+  heads(h_begin + sub, a, d);
+  const int64_t pos = t.rope ? t.positions[r] : 0;
   const int32_t s = seq_of_row(b, (int32_t)r);
   if (s < 0) return;
   const Seq sq = load_seq(b, (uint32_t)s);
   const int32_t at = sq.first + ((int32_t)r - sq.row0);
-  bool placed = at >= 0 && at < sq.n_keys;
-  const int64_t pos = t.rope ? t.positions[r] : 0;
+  bool placed = at >= 0 && at < sq.n_keys && (!t.rope || (pos >= 0 && (uint64_t)pos < t.n_positions));
   if (placed) {
     const int32_t id = b.table[(uint64_t)s * b.table_stride + cache.page.div((uint32_t)at)];
-    placed = id >= 0 && (uint32_t)id < cache.n_pages && (!t.rope || (pos >= 0 && (uint64_t)pos < t.n_positions));
+    placed = id >= 0 && (uint32_t)id < cache.n_pages;
   }
   float co[8], si[8];
   if (placed && t.rope && p.turns) load_turn(t, p, (uint64_t)pos, co, si);
@@ -266,16 +278,9 @@ __global__ __launch_bounds__(256) void k_kv8_append(Cache8 cache, Batch b, Rows 
     if (p.has0) w[0] = load_row8(q_norm + p.c0 * 8);
     if (p.has1) w[1] = load_row8(q_norm + p.c1 * 8);
   }
-  const uint32_t per_part = (q.n_heads + parts - 1) / parts;
-  const uint32_t h_end = min((part + 1) * per_part, q.n_heads);
-  for (uint32_t h0 = part * per_part; h0 < h_end; h0 += HW) {
-    const uint32_t h = h0 + sub;
-    const bool on = h < h_end, reads = on && placed;
-    const T* src = (const T*)q.p + r * q.token_stride + (uint64_t)h * q.head_stride;
-    T* dst = (T*)q_out.p + r * q_out.token_stride + (uint64_t)h * q_out.head_stride;
-    v8 a = {}, d = {};
-    if (reads && p.has0) a = load_row8(src + p.c0 * 8);
-    if (reads && p.has1) d = load_row8(src + p.c1 * 8);
+  for (uint32_t h = h_begin + sub; h - sub < h_end; h += HW) {
+    v8 next_a, next_d;
+    heads(h + HW, next_a, next_d);
     if (q_norm || t.rope) {
       float x[8], y[8];
 #pragma unroll
@@ -283,10 +288,13 @@ __global__ __launch_bounds__(256) void k_kv8_append(Cache8 cache, Batch b, Rows 
       turn<T, L>(t, p, q_norm != nullptr, w, placed && t.rope, co, si, x, y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) a[e] = (T)x[e], d[e] = (T)y[e];
-      if (!placed) a = d = v8{};
     }
-    if (on && p.has0) *(v8*)(dst + p.c0 * 8) = a;
-    if (on && p.has1) *(v8*)(dst + p.c1 * 8) = d;
+    if (!placed) a = d = v8{};
+    T* dst = (T*)q_out.p + r * q_out.token_stride + (uint64_t)h * q_out.head_stride;
+    if (h < h_end && p.has0) *(v8*)(dst + p.c0 * 8) = a;
+    if (h < h_end && p.has1) *(v8*)(dst + p.c1 * 8) = d;
+    a = next_a;
+    d = next_d;
   }
 }
 
