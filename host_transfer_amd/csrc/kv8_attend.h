@@ -6,9 +6,13 @@
 namespace ibp {
 namespace kv {
 
-hipError_t launch_decode8(const AttendPlan& p, const Cache8& c, uint32_t dtype, const Batch& b,
-                          const Rows& q, const Rows& out, float scale, uint32_t window, bool causal,
-                          float* lse, Partial part, hipStream_t s);
+// Workgroups of k_kv8_decode that a CU runs at a time, by its registers (columns of 16 rows).
+constexpr uint32_t decode8_groups(uint32_t head_dim, uint32_t columns) {
+  return head_dim <= 128 ? (columns == 1 ? 4 : 2) : (columns == 1 ? 2 : 1);
+}
+hipError_t launch_decode8(const AttendPlan& p, uint32_t columns, const Cache8& c, uint32_t dtype,
+                          const Batch& b, const Rows& q, const Rows& out, float scale, uint32_t window,
+                          bool causal, float* lse, Partial part, hipStream_t s);
 hipError_t launch_chunk8(const AttendPlan& p, const Cache8& c, uint32_t dtype, const Batch& b,
                          const Rows& q, const Rows& out, float scale, uint32_t window, bool causal,
                          float* lse, Partial part, hipStream_t s);

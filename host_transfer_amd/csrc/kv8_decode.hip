@@ -11,15 +11,15 @@ namespace {
 constexpr int kTile = 32;   // keys of a wave's step
 constexpr int kWaves = 4;
 
-// As k_kv_decode: a workgroup per (up to 16 rows that share a key head, split of their keys), its four waves
+// As k_kv_decode: a workgroup per (up to 16 NC rows that share a key head, split of their keys), its four waves
 // over four key heads of the same tokens or over one head's keys in turn, each with a running maximum
 // and sum of its own.  A wave reads 32 keys' codes of K and of V at a time, neighbouring lanes
 // neighbouring pieces of 16 codes, makes 16-bit rows of them in its registers (two codes an instruction,
 // which applies the block's power of two too) and passes those through its own part of LDS, K first,
 // then V in its place: the first product reads rows, the second one transposed.
 // Bound by the reading of K and V, 2 * D bytes a key.
-template <typename T, int DP, int kHeads>
-__global__ __launch_bounds__(256, 1) void k_kv8_decode(
+template <typename T, int DP, int kHeads, int NC>  // NC: columns of 16 rows
+__global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
     Cache8 cache, Batch b, Rows q, Rows out, float scale_log2, uint32_t window, bool causal,
     uint32_t row_tiles, Partial part, float* __restrict__ lse) {
   constexpr int KS = DP / 32;   // products of the scores
@@ -52,22 +52,14 @@ __global__ __launch_bounds__(256, 1) void k_kv8_decode(
   const Seq sq = load_seq(b, s);
   // rows of this tile: m = i * group + g, [m0, m1)
   const uint32_t n_m = (uint32_t)max(sq.q_len, 0) * group;
-  const uint32_t m0 = tile * 16;
+  const uint32_t m0 = tile * (16 * NC);
   if (m0 >= n_m) return;
-  const uint32_t m1 = min(m0 + 16, n_m);
-  const bool have = m0 + col < m1;
-  const uint32_t m = have ? m0 + col : m1 - 1;
-  const int32_t i = (int32_t)(m / group);
-  const uint32_t head = kh * group + m % group;
-  const uint32_t row = (uint32_t)(sq.row0 + i);
+  const uint32_t m1 = min(m0 + 16 * NC, n_m);
 
-  // keys that this lane's row sees, [lo, hi), and those that any row of the tile sees
-  const int32_t pos = max(sq.first + i, -1);
+  // keys that any row of the tile sees
   const int32_t pos_a = max(sq.first + (int32_t)(m0 / group), -1);
   const int32_t pos_e = max(sq.first + (int32_t)((m1 - 1) / group), -1);
   const int32_t w = (int32_t)window;
-  const int32_t lo = w ? max(pos - w + 1, 0) : 0;
-  const int32_t hi = causal ? min(pos + 1, sq.n_keys) : sq.n_keys;
   const int32_t lo_a = w ? max(pos_a - w + 1, 0) : 0;   // least lo
   const int32_t lo_e = w ? max(pos_e - w + 1, 0) : 0;   // greatest
   const int32_t hi_a = causal ? min(pos_a + 1, sq.n_keys) : sq.n_keys;  // least hi
@@ -80,41 +72,55 @@ __global__ __launch_bounds__(256, 1) void k_kv8_decode(
   const int32_t begin = from + min((int32_t)split * per, tiles) * kBlockKeys;
   const int32_t end = min(from + min(((int32_t)split + 1) * per, tiles) * kBlockKeys, hi_e);
 
-  const T* qp = (const T*)q.p + row * q.token_stride + (uint64_t)head * q.head_stride;
+  // of this lane's rows, one in each column: queries, keys seen [lo, hi)
   const T* zeros = (const T*)zero_row;
-  V8<T> qf[KS];
+  V8<T> qf[NC][KS];
+  int32_t lo[NC], hi[NC];
 #pragma unroll
-  for (int k = 0; k < KS; ++k) {
-    const uint32_t c = (k * 4 + quarter) * 8;
-    qf[k] = load_row8(have && c < hd ? qp + c : zeros);
+  for (int n = 0; n < NC; ++n) {
+    const bool have = m0 + n * 16 + col < m1;
+    const uint32_t m = have ? m0 + n * 16 + col : m1 - 1;
+    const int32_t i = (int32_t)(m / group);
+    const int32_t pos = max(sq.first + i, -1);
+    lo[n] = w ? max(pos - w + 1, 0) : 0;
+    hi[n] = causal ? min(pos + 1, sq.n_keys) : sq.n_keys;
+    const T* qp = (const T*)q.p + (uint32_t)(sq.row0 + i) * q.token_stride +
+                  (uint64_t)(kh * group + m % group) * q.head_stride;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const uint32_t c = (k * 4 + quarter) * 8;
+      qf[n][k] = load_row8(have && c < hd ? qp + c : zeros);
+    }
   }
 
-  f32x4 o[DT];
+  f32x4 o[NC][DT];
+  float top[NC], z[NC];
 #pragma unroll
-  for (int t = 0; t < DT; ++t) o[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float top = -INFINITY, z = 0.f;
+  for (int n = 0; n < NC; ++n) {
+    top[n] = -INFINITY;
+    z[n] = 0.f;
+#pragma unroll
+    for (int t = 0; t < DT; ++t) o[n][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
 
   const int32_t* table = b.table + (uint64_t)s * b.table_stride;
   const uint8_t* kbase = cache.k + (uint64_t)kh * cache.head_stride;
   const uint8_t* vbase = cache.v + (uint64_t)kh * cache.head_stride;
   T* sv = (T*)s_v[wave];
 
-  // Where key t0 + lane % 32 lies (bytes) and its block's exponents (of K, of V); bit r of the
-  // result: some row sees key t0 + r.
-  auto locate = [&](int32_t t0, uint64_t& at, uint32_t& ke, uint32_t& ve) -> uint32_t {
+  // page id of key t0 + lane % 32 (-1: no row sees it)
+  auto lookup = [&](int32_t t0) -> int32_t {
     const int32_t j = t0 + (int32_t)(lane % kTile);
-    bool see = j < end && j >= lo_a;
-    int32_t id = -1;
-    uint32_t page = 0;
-    if (see) {
-      page = cache.page.div((uint32_t)j);
-      id = table[page];
-    }
-    see = id >= 0 && (uint32_t)id < cache.n_pages;
+    return j < end && j >= lo_a ? table[cache.page.div((uint32_t)j)] : -1;
+  };
+  // Where that key lies (bytes) and its block's exponents (of K, of V); bit r of the result: some
+  // row sees key t0 + r.
+  auto locate = [&](int32_t t0, int32_t id, uint64_t& at, uint32_t& ke, uint32_t& ve) -> uint32_t {
+    const bool see = id >= 0 && (uint32_t)id < cache.n_pages;
     at = 0;
     ke = ve = 0;
     if (see) {
-      const uint32_t in = (uint32_t)j - page * cache.page.d;
+      const uint32_t j = (uint32_t)t0 + lane % kTile, in = j - cache.page.div(j) * cache.page.d;
       at = (uint64_t)(uint32_t)id * cache.page_stride + (uint64_t)in * cache.token_stride;
       const uint64_t e = ((uint64_t)(uint32_t)id * cache.page_blocks + cache.block.div(in)) * cache.n_heads + kh;
       ke = cache.k_exp[e];
@@ -140,11 +146,14 @@ __global__ __launch_bounds__(256, 1) void k_kv8_decode(
   const T* tr_at = sv + (4 * quarter + col / 4) * LD + 4 * (col % 4);
   bool odd = false;  // values that only some rows see and that are no numbers were left out
 
-  for (int32_t t0 = begin + (int32_t)(wave / kHeads) * kTile; t0 < end; t0 += kBlockKeys) {
+  const int32_t first = begin + (int32_t)(wave / kHeads) * kTile;
+  int32_t id = lookup(first);
+  for (int32_t t0 = first; t0 < end; t0 += kBlockKeys) {
     uint4 kc[NL], vc[NL];
     uint64_t at;
     uint32_t ke, ve;
-    const uint32_t there = locate(t0, at, ke, ve);
+    const uint32_t there = locate(t0, id, at, ke, ve);
+    id = lookup(t0 + kBlockKeys);  // (a step ahead: the rows' requests wait for nothing)
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const uint64_t from_base = offset(at, i);
@@ -164,15 +173,20 @@ __global__ __launch_bounds__(256, 1) void k_kv8_decode(
       *(V8<T>*)(to + 8) = Read8<T>::eight(kc[i].z, kc[i].w, p);
     }
     wave_sync();
-    f32x4 sc[2];
+    f32x4 sc[NC][2];
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-      sc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
-        sc[a] = mfma16(*(const V8<T>*)(k_at + a * 16 * LD + k * 32), qf[k], sc[a]);
+      for (int n = 0; n < NC; ++n) sc[n][a] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const V8<T> kf = *(const V8<T>*)(k_at + a * 16 * LD + k * 32);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) sc[n][a] = mfma16(kf, qf[n][k], sc[n][a]);
+      }
     }
-    settle(sc[0], sc[1]);
+#pragma unroll
+    for (int n = 0; n < NC; ++n) settle(sc[n][0], sc[n][1]);
     // V in its place
     wave_sync();
 #pragma unroll
@@ -193,61 +207,72 @@ __global__ __launch_bounds__(256, 1) void k_kv8_decode(
     }
 
     // lane's scores: keys t0 + 16 a + 4 quarter + r of its column's row
-    float x[8];
+    V8<T> p[NC];
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x[a * 4 + r] = sc[a][r] * scale_log2;
-    if (!plain) {
+    for (int n = 0; n < NC; ++n) {
+      float x[8];
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t kk = 4 * quarter + r;
-          const int32_t j = t0 + a * 16 + (int32_t)kk;
-          if (!((there >> (a * 16 + kk)) & 1u) || j < lo || j >= hi) x[a * 4 + r] = -INFINITY;
-        }
-    }
-    float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
-                       fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    most = max_half(max_quarter(most));
-    // (any new maximum, as in k_kv_decode: its weight is then 2^kLift and rounds to itself)
-    if (__any(most > top + Base<In8<T>>::kLift)) {
-      const float next = next_base<In8<T>>(top, most);
-      const float keep = exp2_raw(top - (next == -INFINITY ? 0.f : next));
-      z *= keep;
+        for (int r = 0; r < 4; ++r) x[a * 4 + r] = sc[n][a][r] * scale_log2;
+      if (!plain) {
 #pragma unroll
-      for (int t = 0; t < DT; ++t)
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[t][r] *= keep;
-      top = next;
-    }
-    const float base = top == -INFINITY ? 0.f : top;
-    V8<T> p;
+          for (int r = 0; r < 4; ++r) {
+            const uint32_t kk = 4 * quarter + r;
+            const int32_t j = t0 + a * 16 + (int32_t)kk;
+            if (!((there >> (a * 16 + kk)) & 1u) || j < lo[n] || j >= hi[n]) x[a * 4 + r] = -INFINITY;
+          }
+      }
+      float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])),
+                         fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+      most = max_half(max_quarter(most));
+      // (any new maximum, as in k_kv_decode: its weight is then 2^kLift and rounds to itself)
+      if (__any(most > top[n] + Base<In8<T>>::kLift)) {
+        const float next = next_base<In8<T>>(top[n], most);
+        const float keep = exp2_raw(top[n] - (next == -INFINITY ? 0.f : next));
+        z[n] *= keep;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+        for (int t = 0; t < DT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[n][t][r] *= keep;
+        top[n] = next;
+      }
+      const float base = top[n] == -INFINITY ? 0.f : top[n];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
 // (the product rounded as the base was: the largest of huge scores, too, is the base itself)
 #pragma clang fp contract(off)
-      const float y = exp2_raw(x[e] - base);
-      z += y;
-      p[e] = (T)y;  // half a step of the dtype, relative, as the output's own rounding
+        const float y = exp2_raw(x[e] - base);
+        z[n] += y;
+        p[n][e] = (T)y;  // half a step of the dtype, relative, as the output's own rounding
+      }
     }
     wave_sync();
 #pragma unroll
-    for (int t = 0; t < DT; ++t)
-      o[t] = mfma16(join<T>(read_tr(tr_at + t * 16), read_tr(tr_at + t * 16 + 16 * LD)), p, o[t]);
+    for (int t = 0; t < DT; ++t) {
+      const V8<T> vf = join<T>(read_tr(tr_at + t * 16), read_tr(tr_at + t * 16 + 16 * LD));
+#pragma unroll
+      for (int n = 0; n < NC; ++n) o[n][t] = mfma16(vf, p[n], o[n][t]);
+    }
     wave_sync();
   }
 
-  settle(o);
-  const bool all = __any(probe(o) != 0.f);  // (of every tile, else of those that some rows do not see)
+  float bad = 0.f;
+#pragma unroll
+  for (int n = 0; n < NC; ++n) {
+    settle(o[n]);
+    bad += probe(o[n]) != 0.f ? 1.f : 0.f;
+  }
+  const bool all = __any(bad != 0.f);  // (of every tile, else of those that some rows do not see)
   if (all || __any(odd)) {
-    for (int32_t t0 = begin + (int32_t)(wave / kHeads) * kTile; t0 < end; t0 += kBlockKeys) {
+    for (int32_t t0 = first; t0 < end; t0 += kBlockKeys) {
       if (!all && t0 >= lo_e && t0 + kTile <= hi_a) continue;
-      V8<T> sees;
+      V8<T> sees[NC];
       uint64_t at;
       uint32_t ke, ve;
-      const uint32_t there = locate(t0, at, ke, ve);
+      const uint32_t there = locate(t0, lookup(t0), at, ke, ve);
 #pragma unroll
       for (int i = 0; i < NL; ++i) {
         const int32_t mine = t0 + (int32_t)load_row + i * RPL;
@@ -264,105 +289,118 @@ __global__ __launch_bounds__(256, 1) void k_kv8_decode(
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int32_t j = t0 + a * 16 + (int32_t)(4 * quarter) + r;
-          const bool see = ((there >> (a * 16 + 4 * quarter + r)) & 1u) && j >= lo && j < hi;
-          sees[a * 4 + r] = (T)(see ? 1.f : 0.f);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            const bool see = ((there >> (a * 16 + 4 * quarter + r)) & 1u) && j >= lo[n] && j < hi[n];
+            sees[n][a * 4 + r] = (T)(see ? 1.f : 0.f);
+          }
         }
       wave_sync();
 #pragma unroll
       for (int t = 0; t < DT; ++t) {
-        f32x4 n = f32x4{0.f, 0.f, 0.f, 0.f};
-        n = mfma16(join<T>(read_tr(tr_at + t * 16), read_tr(tr_at + t * 16 + 16 * LD)), sees, n);
-        settle(n);
+        const V8<T> vf = join<T>(read_tr(tr_at + t * 16), read_tr(tr_at + t * 16 + 16 * LD));
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[t][r] = add_odd(o[t][r], n[r]);
+        for (int n = 0; n < NC; ++n) {
+          f32x4 count = f32x4{0.f, 0.f, 0.f, 0.f};
+          count = mfma16(vf, sees[n], count);
+          settle(count);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[n][t][r] = add_odd(o[n][t][r], count[r]);
+        }
       }
       wave_sync();
     }
   }
 
-  // the four waves' results together: rows of DP floats in the V tiles
-  z = sum_half(sum_quarter(z));
-  float* so = (float*)s_v[wave];
+  // the four waves' results together, a column of rows at a time: rows of DP floats in the V tiles
 #pragma unroll
-  for (int t = 0; t < DT; ++t) *(f32x4*)(so + col * DP + t * 16 + quarter * 4) = o[t];
-  if (quarter == 0) {
-    s_m[wave][col] = top;
-    s_z[wave][col] = z;
-  }
-  __syncthreads();
-  // a row of a head to 16 / kHeads threads; the head's waves are mine, mine + kHeads, ...
-  constexpr uint32_t kOf = 256 / kHeads, kRowThreads = kOf / 16;
-  const uint32_t mine = threadIdx.x / kOf, r = threadIdx.x % kOf / kRowThreads;
-  const uint32_t first_c = threadIdx.x % kRowThreads;
-  if (m0 + r >= m1) return;
-  float mm = s_m[mine][r];
+  for (int n = 0; n < NC; ++n) {
+    if (n > 0) __syncthreads();
+    const float zn = sum_half(sum_quarter(z[n]));
+    float* so = (float*)s_v[wave];
 #pragma unroll
-  for (int a = 1; a < kTurns; ++a) mm = fmaxf(mm, s_m[mine + a * kHeads][r]);
-  float f[kTurns], zz = 0.f;
+    for (int t = 0; t < DT; ++t) *(f32x4*)(so + col * DP + t * 16 + quarter * 4) = o[n][t];
+    if (quarter == 0) {
+      s_m[wave][col] = top[n];
+      s_z[wave][col] = zn;
+    }
+    __syncthreads();
+    // a row of a head to 16 / kHeads threads; the head's waves are mine, mine + kHeads, ...
+    constexpr uint32_t kOf = 256 / kHeads, kRowThreads = kOf / 16;
+    const uint32_t mine = threadIdx.x / kOf, r = threadIdx.x % kOf / kRowThreads;
+    const uint32_t first_c = threadIdx.x % kRowThreads;
+    const uint32_t rm = m0 + n * 16 + r;
+    if (rm >= m1) continue;
+    float mm = s_m[mine][r];
 #pragma unroll
-  for (int a = 0; a < kTurns; ++a) {
-    f[a] = exp2_raw(s_m[mine + a * kHeads][r] - (mm == -INFINITY ? 0.f : mm));
-    zz += f[a] * s_z[mine + a * kHeads][r];
-  }
-  const uint32_t rm = m0 + r;
-  const uint32_t rrow = (uint32_t)sq.row0 + rm / group;
-  const uint32_t rhead = (kh - wave % kHeads + mine) * group + rm % group;
-  const uint64_t unit = (uint64_t)rrow * q.n_heads + rhead;
-  const bool whole = part.splits == 1;
-  const float inv = zz == 0.f ? 0.f : 1.f / zz;
-  T* op = (T*)out.p + rrow * out.token_stride + (uint64_t)rhead * out.head_stride;
-  for (uint32_t c = first_c; c < hd / 8; c += kRowThreads) {
-    float y[8];
+    for (int a = 1; a < kTurns; ++a) mm = fmaxf(mm, s_m[mine + a * kHeads][r]);
+    float f[kTurns], zz = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      y[e] = 0.f;
+    for (int a = 0; a < kTurns; ++a) {
+      f[a] = exp2_raw(s_m[mine + a * kHeads][r] - (mm == -INFINITY ? 0.f : mm));
+      zz += f[a] * s_z[mine + a * kHeads][r];
+    }
+    const uint32_t rrow = (uint32_t)sq.row0 + rm / group;
+    const uint32_t rhead = (kh - wave % kHeads + mine) * group + rm % group;
+    const uint64_t unit = (uint64_t)rrow * q.n_heads + rhead;
+    const bool whole = part.splits == 1;
+    const float inv = zz == 0.f ? 0.f : 1.f / zz;
+    T* op = (T*)out.p + rrow * out.token_stride + (uint64_t)rhead * out.head_stride;
+    for (uint32_t c = first_c; c < hd / 8; c += kRowThreads) {
+      float y[8];
 #pragma unroll
-      for (int a = 0; a < kTurns; ++a) {
-        const float x = ((const float*)s_v[mine + a * kHeads])[r * DP + c * 8 + e];
-        y[e] += kTurns == 1 ? x : scaled(x, f[a]);
+      for (int e = 0; e < 8; ++e) {
+        y[e] = 0.f;
+#pragma unroll
+        for (int a = 0; a < kTurns; ++a) {
+          const float x = ((const float*)s_v[mine + a * kHeads])[r * DP + c * 8 + e];
+          y[e] += kTurns == 1 ? x : scaled(x, f[a]);
+        }
+        y[e] *= Read8<T>::kScale;
       }
-      y[e] *= Read8<T>::kScale;
-    }
-    if (whole) {
-      V8<T> v;
+      if (whole) {
+        V8<T> v;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = mean<T>(y[e], inv);
-      *(V8<T>*)(op + c * 8) = v;
-    } else {
-      float* to_ = part.row(unit, split) + c * 8;
-      *(f32x4*)to_ = f32x4{y[0], y[1], y[2], y[3]};
-      *(f32x4*)(to_ + 4) = f32x4{y[4], y[5], y[6], y[7]};
+        for (int e = 0; e < 8; ++e) v[e] = mean<T>(y[e], inv);
+        *(V8<T>*)(op + c * 8) = v;
+      } else {
+        float* to_ = part.row(unit, split) + c * 8;
+        *(f32x4*)to_ = f32x4{y[0], y[1], y[2], y[3]};
+        *(f32x4*)(to_ + 4) = f32x4{y[4], y[5], y[6], y[7]};
+      }
     }
-  }
-  if (first_c == 0) {
-    if (!whole) part.ms[unit * part.splits + split] = make_float2(mm, zz);
-    else if (lse) lse[unit] = zz == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(zz)) * kLn2;
+    if (first_c == 0) {
+      if (!whole) part.ms[unit * part.splits + split] = make_float2(mm, zz);
+      else if (lse) lse[unit] = zz == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(zz)) * kLn2;
+    }
   }
 }
 
-template <typename T, int DP, int kHeads>
+template <typename T, int DP, int kHeads, int NC>
 hipError_t run_decode8(const AttendPlan& p, const Cache8& c, const Batch& b, const Rows& q,
                        const Rows& out, float scale, uint32_t window, bool causal, float* lse,
                        Partial part, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv8_decode<T, DP, kHeads>), dim3((uint32_t)p.blocks), dim3(256), 0, s, c, b, q, out,
+  hipLaunchKernelGGL((k_kv8_decode<T, DP, kHeads, NC>), dim3((uint32_t)p.blocks), dim3(256), 0, s, c, b, q, out,
                      scale * kLog2e * Read8<T>::kScale, window, causal, p.row_tiles, part, lse);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_decode8(const AttendPlan& p, const Cache8& c, uint32_t dtype, const Batch& b,
-                          const Rows& q, const Rows& out, float scale, uint32_t window, bool causal,
-                          float* lse, Partial part, hipStream_t s) {
-#define IBP_KV8_DECODE(T, DP, HEADS) \
-  run_decode8<T, DP, HEADS>(p, c, b, q, out, scale, window, causal, lse, part, s)
-#define IBP_KV8_DECODE_T(T, HEADS)                                              \
-  (c.head_dim <= 64    ? IBP_KV8_DECODE(T, 64, HEADS)                           \
-   : c.head_dim <= 128 ? IBP_KV8_DECODE(T, 128, HEADS)                          \
-                       : IBP_KV8_DECODE(T, 256, HEADS))
-#define IBP_KV8_DECODE_S(T) (p.heads == 4 ? IBP_KV8_DECODE_T(T, 4) : IBP_KV8_DECODE_T(T, 1))
+hipError_t launch_decode8(const AttendPlan& p, uint32_t columns, const Cache8& c, uint32_t dtype,
+                          const Batch& b, const Rows& q, const Rows& out, float scale, uint32_t window,
+                          bool causal, float* lse, Partial part, hipStream_t s) {
+#define IBP_KV8_DECODE(T, DP, HEADS, NC) \
+  run_decode8<T, DP, HEADS, NC>(p, c, b, q, out, scale, window, causal, lse, part, s)
+#define IBP_KV8_DECODE_T(T, HEADS, NC)                                              \
+  (c.head_dim <= 64    ? IBP_KV8_DECODE(T, 64, HEADS, NC)                           \
+   : c.head_dim <= 128 ? IBP_KV8_DECODE(T, 128, HEADS, NC)                          \
+                       : IBP_KV8_DECODE(T, 256, HEADS, NC))
+#define IBP_KV8_DECODE_C(T, HEADS) (columns == 2 ? IBP_KV8_DECODE_T(T, HEADS, 2) : IBP_KV8_DECODE_T(T, HEADS, 1))
+#define IBP_KV8_DECODE_S(T) (p.heads == 4 ? IBP_KV8_DECODE_C(T, 4) : IBP_KV8_DECODE_C(T, 1))
   return dtype == IBP_KV_F16 ? IBP_KV8_DECODE_S(_Float16) : IBP_KV8_DECODE_S(__bf16);
 #undef IBP_KV8_DECODE_S
+#undef IBP_KV8_DECODE_C
 #undef IBP_KV8_DECODE_T
 #undef IBP_KV8_DECODE
 }
