@@ -11,17 +11,89 @@ namespace {
 constexpr int kTile = 32;   // keys of a wave's step
 constexpr int kWaves = 4;
 
-// As k_kv_decode: a workgroup per (up to 16 NC rows that share a key head, split of their keys), its four waves
-// over four key heads of the same tokens or over one head's keys in turn, each with a running maximum
+// As k_kv_decode: a workgroup per (up to 16 NC rows that share a key head, split of their keys; all rows of
+// a sequence), its four waves over four key heads of the same tokens or over one head's keys in turn, each with a running maximum
 // and sum of its own.  A wave reads 32 keys' codes of K and of V at a time, neighbouring lanes
 // neighbouring pieces of 16 codes, makes 16-bit rows of them in its registers (two codes an instruction,
 // which applies the block's power of two too) and passes those through its own part of LDS, K first,
 // then V in its place: the first product reads rows, the second one transposed.
 // Bound by the reading of K and V, 2 * D bytes a key.
+// Inclusive prefix sums and the sum over the wave's lanes by lane moves of the vector ALU, a few cycles
+// each (through LDS the shares cost every workgroup about 5 us).
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t moved(uint32_t x) {  // 0 where no lane is moved from
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kCtrl, kRows, 0xf, false);
+}
+__device__ __forceinline__ uint32_t prefix_sum(uint32_t x) {
+  x += moved<0x111, 0xf>(x);  // within rows of 16 lanes, 1, 2, 4 and 8 further
+  x += moved<0x112, 0xf>(x);
+  x += moved<0x114, 0xf>(x);
+  x += moved<0x118, 0xf>(x);
+  x += moved<0x142, 0xa>(x);  // a row's last lane to the next row, the second's to the last two
+  x += moved<0x143, 0xc>(x);
+  return x;
+}
+__device__ __forceinline__ uint32_t wave_sum(uint32_t x) { return lane_u32(prefix_sum(x), kWave - 1); }
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max(x, moved<0x111, 0xf>(x));
+  x = max(x, moved<0x112, 0xf>(x));
+  x = max(x, moved<0x114, 0xf>(x));
+  x = max(x, moved<0x118, 0xf>(x));
+  x = max(x, moved<0x142, 0xa>(x));
+  x = max(x, moved<0x143, 0xc>(x));
+  return lane_u32(x, kWave - 1);
+}
+
+// The sequence and split of workgroup `place` of its head group, and the split's length: with n_s =
+// max(ceil(tiles_s / size), 1) workgroups for a sequence that has rows, size the least length with which
+// all sequences' are at most `shares`; sequences in their order.  s < 0: there is none for it.
+//   mine    2 * tiles + 1 of sequence `lane`, 0 where it has no rows; others', past 64, in `tiles`
+struct Part8 {
+  int32_t s, split, splits, size, place;  // place: the sequence's first workgroup
+};
+__device__ __forceinline__ Part8 part_of(uint32_t mine, const uint32_t* tiles, uint32_t n_seqs, uint32_t shares,
+                                         uint32_t place, uint32_t lane) {
+  auto at = [&](uint32_t j0) -> uint32_t { return j0 == 0 ? mine : j0 + lane < n_seqs ? tiles[j0 + lane] : 0; };
+  uint32_t total = 0, most = 0, active = 0;
+  for (uint32_t j0 = 0; j0 < n_seqs; j0 += kWave) {
+    const uint32_t t = at(j0);
+    total += wave_sum(t >> 1);
+    most = max(most, wave_max(t >> 1));
+    active += (uint32_t)__builtin_popcountll(__ballot(t & 1u));
+  }
+  // lo may be too short, hi is not: sum of ceil(t / hi) <= total / hi + active
+  uint32_t lo = max((total + shares - 1) / shares, 1u), hi = max(most, 1u);
+  if (shares > active) hi = min(hi, (total + shares - active - 1) / (shares - active));
+  hi = max(hi, lo);
+  auto splits = [&](uint32_t t, uint32_t size) { return t ? max(((t >> 1) + size - 1) / size, 1u) : 0u; };
+  while (lo < hi) {
+    const uint32_t mid = (lo + hi) / 2;
+    uint32_t n = 0;
+    for (uint32_t j0 = 0; j0 < n_seqs; j0 += kWave) n += wave_sum(splits(at(j0), mid));
+    if (n <= shares) hi = mid;
+    else lo = mid + 1;
+  }
+  Part8 p = {-1, 0, 0, (int32_t)hi, 0};
+  uint32_t before = 0;
+  for (uint32_t j0 = 0; j0 < n_seqs && p.s < 0; j0 += kWave) {
+    const uint32_t n = splits(at(j0), hi), upto = before + prefix_sum(n);
+    const uint64_t here = __ballot(n && place >= upto - n && place < upto);
+    if (here) {
+      const uint32_t l = (uint32_t)__builtin_ctzll(here);
+      p.s = (int32_t)(j0 + l);
+      p.splits = (int32_t)lane_u32(n, l);
+      p.place = (int32_t)(lane_u32(upto, l) - lane_u32(n, l));
+      p.split = (int32_t)place - p.place;
+    }
+    before = lane_u32(upto, kWave - 1);
+  }
+  return p;
+}
+
 template <typename T, int DP, int kHeads, int NC>  // NC: columns of 16 rows
 __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
     Cache8 cache, Batch b, Rows q, Rows out, float scale_log2, uint32_t window, bool causal,
-    uint32_t row_tiles, Partial part, float* __restrict__ lse) {
+    Plan8 plan, float* __restrict__ lse) {
   constexpr int KS = DP / 32;   // products of the scores
   constexpr int DT = DP / 16;   // tiles of the output
   constexpr int LD = DP + 16;   // LDS row, elements
@@ -39,38 +111,64 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
   const uint32_t group = q.n_heads / cache.n_heads;
   const uint32_t hd = cache.head_dim;
 
-  // block -> (sequence, row tile, split, key head), heads innermost: the heads of a token lie
-  // side by side in memory
-  uint32_t u = blockIdx.x;
+  // block -> (its place among the head's workgroups, key head), heads innermost: the heads of a
+  // token lie side by side in memory
   const uint32_t head_blocks = cache.n_heads / kHeads;
-  const uint32_t kh = u % head_blocks * kHeads + wave % kHeads;
-  u /= head_blocks;
-  const uint32_t split = u % part.splits;
-  u /= part.splits;
-  const uint32_t tile = u % row_tiles;
-  const uint32_t s = u / row_tiles;
-  const Seq sq = load_seq(b, s);
-  // rows of this tile: m = i * group + g, [m0, m1)
-  const uint32_t n_m = (uint32_t)max(sq.q_len, 0) * group;
-  const uint32_t m0 = tile * (16 * NC);
-  if (m0 >= n_m) return;
-  const uint32_t m1 = min(m0 + 16 * NC, n_m);
-
-  // keys that any row of the tile sees
-  const int32_t pos_a = max(sq.first + (int32_t)(m0 / group), -1);
-  const int32_t pos_e = max(sq.first + (int32_t)((m1 - 1) / group), -1);
+  const uint32_t kh = blockIdx.x % head_blocks * kHeads + wave % kHeads;
+  const uint32_t place = blockIdx.x / head_blocks;
   const int32_t w = (int32_t)window;
-  const int32_t lo_a = w ? max(pos_a - w + 1, 0) : 0;   // least lo
-  const int32_t lo_e = w ? max(pos_e - w + 1, 0) : 0;   // greatest
-  const int32_t hi_a = causal ? min(pos_a + 1, sq.n_keys) : sq.n_keys;  // least hi
-  const int32_t hi_e = causal ? min(pos_e + 1, sq.n_keys) : sq.n_keys;  // greatest
+  // keys that the first and the last row of a sequence see, [lo, hi); whole tiles of the workgroup
+  auto first_lo = [&](const Seq& sq) { return w ? max(max(sq.first, -1) - w + 1, 0) : 0; };
+  auto last_hi = [&](const Seq& sq) {
+    return causal ? min(max(sq.first + sq.q_len - 1, -1) + 1, sq.n_keys) : sq.n_keys;
+  };
+  auto tiles_of = [&](const Seq& sq) {
+    const int32_t from = first_lo(sq) / kBlockKeys * kBlockKeys;
+    return max(last_hi(sq) - from + kBlockKeys - 1, 0) / kBlockKeys;
+  };
+  Part8 at_ = {(int32_t)place, 0, 1, 0x7FFFFFFF, 0};
+  Seq sq;
+  if (plan.shares) {
+    // sequences past the first 64: their lengths where the rows of V will lie
+    static_assert(kMaxShared <= kWaves * WORDS, "the lengths fit");
+    uint32_t* s_tiles = (uint32_t*)s_v;
+    auto length = [&](const Seq& x) { return x.q_len > 0 ? (uint32_t)tiles_of(x) << 1 | 1u : 0u; };
+    Seq mine = {0, 0, 0, 0};
+    if (lane < b.n_seqs) mine = load_seq(b, lane);
+    if (b.n_seqs > (uint32_t)kWave) {
+      for (uint32_t j = kWave + threadIdx.x; j < b.n_seqs; j += 256) s_tiles[j] = length(load_seq(b, j));
+      __syncthreads();
+    }
+    at_ = part_of(length(mine), s_tiles, b.n_seqs, plan.shares, place, lane);
+    if (b.n_seqs > (uint32_t)kWave) __syncthreads();
+    if (at_.s < 0) return;
+    if (at_.split == 0 && blockIdx.x % head_blocks == 0 && threadIdx.x == 0)
+      plan.heads[at_.s] = make_int2(at_.place, at_.splits);
+    if (at_.s < kWave)
+      sq = Seq{(int32_t)lane_u32((uint32_t)mine.row0, at_.s), (int32_t)lane_u32((uint32_t)mine.q_len, at_.s),
+               (int32_t)lane_u32((uint32_t)mine.first, at_.s), (int32_t)lane_u32((uint32_t)mine.n_keys, at_.s)};
+    else
+      sq = load_seq(b, (uint32_t)at_.s);
+  } else {
+    sq = load_seq(b, place);
+  }
+  const uint32_t s = (uint32_t)at_.s;
+  const uint32_t n_m = (uint32_t)max(sq.q_len, 0) * group;  // rows: m = i * group + g
+  if (n_m == 0) return;
+  const uint32_t m1 = min(n_m, 16u * NC);
+
+  const int32_t pos_e = max(sq.first + sq.q_len - 1, -1);
+  const int32_t lo_a = first_lo(sq);                      // least lo of a row
+  const int32_t lo_e = w ? max(pos_e - w + 1, 0) : 0;     // greatest
+  const int32_t hi_a = causal ? min(max(sq.first, -1) + 1, sq.n_keys) : sq.n_keys;  // least hi
+  const int32_t hi_e = last_hi(sq);                       // greatest
 
   // the split's keys, whole tiles of the workgroup
   const int32_t from = lo_a / kBlockKeys * kBlockKeys;
-  const int32_t tiles = max(hi_e - from + kBlockKeys - 1, 0) / kBlockKeys;
-  const int32_t per = (tiles + (int32_t)part.splits - 1) / (int32_t)part.splits;
-  const int32_t begin = from + min((int32_t)split * per, tiles) * kBlockKeys;
-  const int32_t end = min(from + min(((int32_t)split + 1) * per, tiles) * kBlockKeys, hi_e);
+  const int32_t tiles = tiles_of(sq);
+  const int32_t per = min(at_.size, tiles);
+  const int32_t begin = from + min(at_.split * per, tiles) * kBlockKeys;
+  const int32_t end = min(from + min((at_.split + 1) * per, tiles) * kBlockKeys, hi_e);
 
   // of this lane's rows, one in each column: queries, keys seen [lo, hi)
   const T* zeros = (const T*)zero_row;
@@ -78,8 +176,8 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
   int32_t lo[NC], hi[NC];
 #pragma unroll
   for (int n = 0; n < NC; ++n) {
-    const bool have = m0 + n * 16 + col < m1;
-    const uint32_t m = have ? m0 + n * 16 + col : m1 - 1;
+    const bool have = n * 16 + col < m1;
+    const uint32_t m = have ? n * 16 + col : m1 - 1;
     const int32_t i = (int32_t)(m / group);
     const int32_t pos = max(sq.first + i, -1);
     lo[n] = w ? max(pos - w + 1, 0) : 0;
@@ -329,7 +427,7 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
     constexpr uint32_t kOf = 256 / kHeads, kRowThreads = kOf / 16;
     const uint32_t mine = threadIdx.x / kOf, r = threadIdx.x % kOf / kRowThreads;
     const uint32_t first_c = threadIdx.x % kRowThreads;
-    const uint32_t rm = m0 + n * 16 + r;
+    const uint32_t rm = n * 16 + r;
     if (rm >= m1) continue;
     float mm = s_m[mine][r];
 #pragma unroll
@@ -343,7 +441,9 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
     const uint32_t rrow = (uint32_t)sq.row0 + rm / group;
     const uint32_t rhead = (kh - wave % kHeads + mine) * group + rm % group;
     const uint64_t unit = (uint64_t)rrow * q.n_heads + rhead;
-    const bool whole = part.splits == 1;
+    const bool whole = at_.splits == 1;
+    // of this (place, key head, row)
+    const uint64_t slot = ((uint64_t)place * cache.n_heads + (kh - wave % kHeads + mine)) * plan.rows + rm;
     const float inv = zz == 0.f ? 0.f : 1.f / zz;
     T* op = (T*)out.p + rrow * out.token_stride + (uint64_t)rhead * out.head_stride;
     for (uint32_t c = first_c; c < hd / 8; c += kRowThreads) {
@@ -364,40 +464,181 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
         for (int e = 0; e < 8; ++e) v[e] = mean<T>(y[e], inv);
         *(V8<T>*)(op + c * 8) = v;
       } else {
-        float* to_ = part.row(unit, split) + c * 8;
+        float* to_ = plan.o + slot * hd + c * 8;
         *(f32x4*)to_ = f32x4{y[0], y[1], y[2], y[3]};
         *(f32x4*)(to_ + 4) = f32x4{y[4], y[5], y[6], y[7]};
       }
     }
     if (first_c == 0) {
-      if (!whole) part.ms[unit * part.splits + split] = make_float2(mm, zz);
+      if (!whole) plan.ms[slot] = make_float2(mm, zz);
       else if (lse) lse[unit] = zz == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(zz)) * kLn2;
     }
   }
 }
 
+// A split row's place in the workspace: its first partial result, how many there are and how far apart;
+// n <= 1: the row is whole, or no sequence's.
+struct Parts8 {
+  uint64_t slot, step;
+  uint32_t n;
+};
+__device__ __forceinline__ Parts8 parts_of(const Batch& b, const Rows& out, const Plan8& plan, uint32_t n_heads,
+                                           uint32_t row, uint32_t head) {
+  const int32_t s = seq_of_row(b, (int32_t)row);
+  if (s < 0) return Parts8{0, 0, 0};
+  const int2 of = plan.heads[s];
+  const uint32_t group = out.n_heads / n_heads;
+  const uint32_t i = row - (uint32_t)load_seq(b, (uint32_t)s).row0;
+  Parts8 p;
+  p.n = (uint32_t)of.y;
+  p.step = (uint64_t)n_heads * plan.rows;
+  p.slot = (uint64_t)of.x * p.step + (uint64_t)(head / group) * plan.rows + i * group + head % group;
+  return p;
+}
+template <typename T>
+__device__ __forceinline__ void finish(const Rows& out, uint32_t row, uint32_t head, uint32_t c, bool live,
+                                       const f32x4& o, float z, float mm, float* lse) {
+  if (live) {
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    t4 v;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = mean<T>(o[r], inv);
+    *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
+  }
+  if (lse && c == 0)
+    lse[(uint64_t)row * out.n_heads + head] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
+}
+
+// The splits of a row together, a wave per (row, head): 64 splits' factors in its lanes, then `lanes` lanes
+// (four channels each) a split.  3,840 rows and heads of about 10 splits 12 us with a workgroup each.
+template <typename T>
+__global__ __launch_bounds__(256) void k_kv8_join(Batch b, Rows out, Plan8 plan, uint32_t n_heads,
+                                                  uint32_t head_dim, uint32_t lanes, float* __restrict__ lse) {
+  const uint32_t lane = threadIdx.x % kWave;
+  const uint64_t unit = (uint64_t)blockIdx.x * 4 + uniform(threadIdx.x / kWave);
+  if (unit >= (uint64_t)b.n_rows * out.n_heads) return;
+  const uint32_t row = (uint32_t)(unit / out.n_heads), head = (uint32_t)(unit % out.n_heads);
+  const Parts8 p = parts_of(b, out, plan, n_heads, row, head);
+  if (p.n <= 1) return;
+  float mm = -INFINITY;
+  for (uint32_t e = lane; e < p.n; e += kWave) mm = fmaxf(mm, plan.ms[p.slot + e * p.step].x);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
+  const float base = mm == -INFINITY ? 0.f : mm;
+  const uint32_t c = lane % lanes * 4, sub = lane / lanes, at_once = kWave / lanes;
+  const bool live = c < head_dim;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  float z = 0.f;
+  for (uint32_t e0 = 0; e0 < p.n; e0 += kWave) {
+    const float2 x = e0 + lane < p.n ? plan.ms[p.slot + (e0 + lane) * p.step] : make_float2(-INFINITY, 0.f);
+    const float f = exp2_raw(x.x - base);
+    z += f * x.y;
+    const uint32_t n = min(p.n - e0, (uint32_t)kWave);
+#pragma unroll 4
+    for (uint32_t e = 0; e < n; e += at_once) {
+      const float fe = __shfl(f, (int)min(e + sub, (uint32_t)kWave - 1));
+      if (!live || e + sub >= n) continue;
+      const f32x4 y = *(const f32x4*)(plan.o + (p.slot + (e0 + e + sub) * p.step) * head_dim + c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += scaled(y[r], fe);
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) z += __shfl_xor(z, d);
+  for (uint32_t d = lanes; d < (uint32_t)kWave; d <<= 1)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] += __shfl_xor(o[r], (int)d);
+  finish<T>(out, row, head, c, live && sub == 0, o, z, mm, sub == 0 ? lse : nullptr);
+}
+
+// The same with a workgroup of 1024 for each (row, head), where the splits are many (128 rows and heads of 128
+// splits 8 us).
+template <typename T>
+__global__ __launch_bounds__(1024) void k_kv8_join_many(Batch b, Rows out, Plan8 plan, uint32_t n_heads,
+                                                       uint32_t head_dim, uint32_t lanes,
+                                                       float* __restrict__ lse) {
+  constexpr uint32_t kThreads = 1024, NW = kThreads / kWave;
+  static_assert(kMaxSplits <= kThreads, "a thread per split");
+  __shared__ float s_f[kThreads];
+  __shared__ float s_red[NW];
+  __shared__ f32x4 s_o[kThreads];
+  const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const uint32_t row = blockIdx.x / out.n_heads, head = blockIdx.x % out.n_heads;
+  const Parts8 p = parts_of(b, out, plan, n_heads, row, head);
+  if (p.n <= 1) return;
+  const float2 x = tid < p.n ? plan.ms[p.slot + tid * p.step] : make_float2(-INFINITY, 0.f);
+  float mm = x.x;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d, kWave));
+  if (lane == 0) s_red[wave] = mm;
+  __syncthreads();
+  for (uint32_t w = 0; w < NW; ++w) mm = fmaxf(mm, s_red[w]);
+  __syncthreads();
+  const float f = exp2_raw(x.x - (mm == -INFINITY ? 0.f : mm));
+  s_f[tid] = f;
+  float z = tid < p.n ? f * x.y : 0.f;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) z += __shfl_xor(z, d, kWave);
+  if (lane == 0) s_red[wave] = z;
+  __syncthreads();
+  z = 0.f;
+  for (uint32_t w = 0; w < NW; ++w) z += s_red[w];
+  const uint32_t c = (tid % lanes) * 4, at_once = kThreads / lanes;
+  const bool live = c < head_dim;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (live) {
+#pragma unroll 4
+    for (uint32_t e = tid / lanes; e < p.n; e += at_once) {
+      const f32x4 y = *(const f32x4*)(plan.o + (p.slot + e * p.step) * head_dim + c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += scaled(y[r], s_f[e]);
+    }
+  }
+  s_o[tid] = o;
+  __syncthreads();
+  for (uint32_t half = kThreads / 2; half >= lanes; half /= 2) {
+    if (tid < half) {
+      const f32x4 y = s_o[tid + half];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] += y[r];
+      s_o[tid] = o;
+    }
+    __syncthreads();
+  }
+  if (tid < lanes) finish<T>(out, row, head, c, live, o, z, mm, lse);
+}
+
 template <typename T, int DP, int kHeads, int NC>
-hipError_t run_decode8(const AttendPlan& p, const Cache8& c, const Batch& b, const Rows& q,
-                       const Rows& out, float scale, uint32_t window, bool causal, float* lse,
-                       Partial part, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv8_decode<T, DP, kHeads, NC>), dim3((uint32_t)p.blocks), dim3(256), 0, s, c, b, q, out,
-                     scale * kLog2e * Read8<T>::kScale, window, causal, p.row_tiles, part, lse);
+hipError_t run_decode8(const Plan8& p, const Cache8& c, const Batch& b, const Rows& q, const Rows& out,
+                       float scale, uint32_t window, bool causal, float* lse, hipStream_t s) {
+  hipLaunchKernelGGL((k_kv8_decode<T, DP, kHeads, NC>), dim3(p.places * (c.n_heads / kHeads)), dim3(256), 0, s,
+                     c, b, q, out, scale * kLog2e * Read8<T>::kScale, window, causal, p, lse);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.shares == 0) return e;
+  const uint32_t lanes = c.head_dim <= 64 ? 16 : c.head_dim <= 128 ? 32 : 64;
+  const uint32_t units = b.n_rows * q.n_heads;
+  if (p.wide_join)
+    hipLaunchKernelGGL(k_kv8_join_many<T>, dim3(units), dim3(1024), 0, s, b, out, p, c.n_heads, c.head_dim, lanes, lse);
+  else
+    hipLaunchKernelGGL(k_kv8_join<T>, dim3((units + 3) / 4), dim3(256), 0, s, b, out, p, c.n_heads, c.head_dim, lanes,
+                       lse);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_decode8(const AttendPlan& p, uint32_t columns, const Cache8& c, uint32_t dtype,
-                          const Batch& b, const Rows& q, const Rows& out, float scale, uint32_t window,
-                          bool causal, float* lse, Partial part, hipStream_t s) {
+hipError_t launch_decode8(const Plan8& p, const Cache8& c, uint32_t dtype, const Batch& b, const Rows& q,
+                          const Rows& out, float scale, uint32_t window, bool causal, float* lse,
+                          hipStream_t s) {
 #define IBP_KV8_DECODE(T, DP, HEADS, NC) \
-  run_decode8<T, DP, HEADS, NC>(p, c, b, q, out, scale, window, causal, lse, part, s)
+  run_decode8<T, DP, HEADS, NC>(p, c, b, q, out, scale, window, causal, lse, s)
 #define IBP_KV8_DECODE_T(T, HEADS, NC)                                              \
   (c.head_dim <= 64    ? IBP_KV8_DECODE(T, 64, HEADS, NC)                           \
    : c.head_dim <= 128 ? IBP_KV8_DECODE(T, 128, HEADS, NC)                          \
                        : IBP_KV8_DECODE(T, 256, HEADS, NC))
-#define IBP_KV8_DECODE_C(T, HEADS) (columns == 2 ? IBP_KV8_DECODE_T(T, HEADS, 2) : IBP_KV8_DECODE_T(T, HEADS, 1))
-#define IBP_KV8_DECODE_S(T) (p.heads == 4 ? IBP_KV8_DECODE_C(T, 4) : IBP_KV8_DECODE_C(T, 1))
+#define IBP_KV8_DECODE_C(T, HEADS) (p.rows > 16 ? IBP_KV8_DECODE_T(T, HEADS, 2) : IBP_KV8_DECODE_T(T, HEADS, 1))
+#define IBP_KV8_DECODE_S(T) (p.head_group == 4 ? IBP_KV8_DECODE_C(T, 4) : IBP_KV8_DECODE_C(T, 1))
   return dtype == IBP_KV_F16 ? IBP_KV8_DECODE_S(_Float16) : IBP_KV8_DECODE_S(__bf16);
 #undef IBP_KV8_DECODE_S
 #undef IBP_KV8_DECODE_C
