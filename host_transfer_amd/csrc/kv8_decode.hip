@@ -245,20 +245,36 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
   bool odd = false;  // values that only some rows see and that are no numbers were left out
 
   const int32_t first = begin + (int32_t)(wave / kHeads) * kTile;
+  // a tile's codes, its blocks' exponents, which of its keys are there
+  struct Tile {
+    uint4 k[NL], v[NL];
+    uint32_t ke, ve, there;
+  };
+  // With two columns the next tile's codes are on their way while this one is computed (24 requests of 5
+  // drafted tokens 74 -> 68 us); with one, four workgroups a CU do better than three that do so (87 and 95).
+  constexpr bool kAhead = NC == 2 && DP <= 128;
+  // page ids are looked up a step ahead: the rows' requests wait for nothing
   int32_t id = lookup(first);
-  for (int32_t t0 = first; t0 < end; t0 += kBlockKeys) {
-    uint4 kc[NL], vc[NL];
+  auto fetch = [&](int32_t t0, Tile& to) {
     uint64_t at;
-    uint32_t ke, ve;
-    const uint32_t there = locate(t0, id, at, ke, ve);
-    id = lookup(t0 + kBlockKeys);  // (a step ahead: the rows' requests wait for nothing)
+    to.there = locate(t0, id, at, to.ke, to.ve);
+    if (!kAhead) id = lookup(t0 + kBlockKeys);
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
       const uint64_t from_base = offset(at, i);
-      const bool on = loads(there, i);
-      kc[i] = codes(on ? kbase + from_base : (const uint8_t*)zeros);
-      vc[i] = codes(on ? vbase + from_base : (const uint8_t*)zeros);
+      const bool on = loads(to.there, i);
+      to.k[i] = codes(on ? kbase + from_base : (const uint8_t*)zeros);
+      to.v[i] = codes(on ? vbase + from_base : (const uint8_t*)zeros);
     }
+    if (kAhead) id = lookup(t0 + kBlockKeys);
+  };
+  Tile now, next;
+  if (kAhead) fetch(first, now);
+  for (int32_t t0 = first; t0 < end; t0 += kBlockKeys) {
+    if (kAhead) fetch(t0 + kBlockKeys, next);
+    else fetch(t0, now);
+    const uint4 (&kc)[NL] = now.k, (&vc)[NL] = now.v;
+    const uint32_t there = now.there, ke = now.ke, ve = now.ve;
     // every row sees every key of the tile?
     const bool plain = there == ~0u && t0 >= lo_e && t0 + kTile <= hi_a;
 
@@ -355,6 +371,7 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
       for (int n = 0; n < NC; ++n) o[n][t] = mfma16(vf, p[n], o[n][t]);
     }
     wave_sync();
+    if (kAhead) now = next;
   }
 
   float bad = 0.f;
