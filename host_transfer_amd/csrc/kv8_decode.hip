@@ -18,32 +18,6 @@ constexpr int kWaves = 4;
 // which applies the block's power of two too) and passes those through its own part of LDS, K first,
 // then V in its place: the first product reads rows, the second one transposed.
 // Bound by the reading of K and V, 2 * D bytes a key.
-// Inclusive prefix sums and the sum over the wave's lanes by lane moves of the vector ALU, a few cycles
-// each (through LDS the shares cost every workgroup about 5 us).
-template <int kCtrl, int kRows>
-__device__ __forceinline__ uint32_t moved(uint32_t x) {  // 0 where no lane is moved from
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kCtrl, kRows, 0xf, false);
-}
-__device__ __forceinline__ uint32_t prefix_sum(uint32_t x) {
-  x += moved<0x111, 0xf>(x);  // within rows of 16 lanes, 1, 2, 4 and 8 further
-  x += moved<0x112, 0xf>(x);
-  x += moved<0x114, 0xf>(x);
-  x += moved<0x118, 0xf>(x);
-  x += moved<0x142, 0xa>(x);  // a row's last lane to the next row, the second's to the last two
-  x += moved<0x143, 0xc>(x);
-  return x;
-}
-__device__ __forceinline__ uint32_t wave_sum(uint32_t x) { return lane_u32(prefix_sum(x), kWave - 1); }
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-  x = max(x, moved<0x111, 0xf>(x));
-  x = max(x, moved<0x112, 0xf>(x));
-  x = max(x, moved<0x114, 0xf>(x));
-  x = max(x, moved<0x118, 0xf>(x));
-  x = max(x, moved<0x142, 0xa>(x));
-  x = max(x, moved<0x143, 0xc>(x));
-  return lane_u32(x, kWave - 1);
-}
-
 // The sequence and split of workgroup `place` of its head group, and the split's length: with n_s =
 // max(ceil(tiles_s / size), 1) workgroups for a sequence that has rows, size the least length with which
 // all sequences' are at most `shares`; sequences in their order.  s < 0: there is none for it.
@@ -76,7 +50,7 @@ __device__ __forceinline__ Part8 part_of(uint32_t mine, const uint32_t* tiles, u
   Part8 p = {-1, 0, 0, (int32_t)hi, 0};
   uint32_t before = 0;
   for (uint32_t j0 = 0; j0 < n_seqs && p.s < 0; j0 += kWave) {
-    const uint32_t n = splits(at(j0), hi), upto = before + prefix_sum(n);
+    const uint32_t n = splits(at(j0), hi), upto = before + wave_prefix_sum(n);
     const uint64_t here = __ballot(n && place >= upto - n && place < upto);
     if (here) {
       const uint32_t l = (uint32_t)__builtin_ctzll(here);

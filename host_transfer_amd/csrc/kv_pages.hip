@@ -7,8 +7,8 @@ namespace kv {
 
 namespace {
 
-constexpr uint32_t kThreads = 1024;     // of the workgroup that looks at the requests, one each
-constexpr uint32_t kWaves = kThreads / kWave;
+constexpr uint32_t kMostThreads = 1024; // of the workgroup that looks at the requests, one each
+constexpr uint32_t kFewThreads = 256;   // of a step of at most as many requests and four times as many rows
 constexpr uint32_t kOneRows = 4096;     // rows that this workgroup writes by itself
 constexpr uint32_t kSearch = 4096;      // requests whose q_start a workgroup holds in LDS
 
@@ -24,31 +24,30 @@ struct Gift {
   int32_t wanted, n;
 };
 
+// Sums that stay at 2^32 - 1 where they would pass it: whatever is compared with them is smaller.
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return __builtin_elementwise_add_sat(a, b); }
+
 // Exclusive prefix sums over the workgroup's threads; the sums of all in `all`.
-template <int N>
-__device__ __forceinline__ void scan(uint64_t (&v)[N], uint64_t (&all)[N], uint64_t (*s)[N]) {
+template <int N, uint32_t kThreads>
+__device__ __forceinline__ void scan(uint32_t (&v)[N], uint32_t (&all)[N], uint32_t (*s)[2]) {
   const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  uint64_t x[N];
+  uint32_t before[N];  // of the wave's lanes before this one
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    x[i] = v[i];
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const uint64_t y = __shfl_up(x[i], d, kWave);
-      if (lane >= (uint32_t)d) x[i] += y;
-    }
-    if (lane == kWave - 1) s[wave][i] = x[i];
+    const uint32_t x = wave_prefix(v[i], [](uint32_t a, uint32_t b) { return add_sat(a, b); });
+    before[i] = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x138, 0xf, 0xf, false);  // the lane before
+    if (lane == kWave - 1) s[wave][i] = x;
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    uint64_t before = 0, total = 0;
-    for (uint32_t w = 0; w < kWaves; ++w) {
-      const uint64_t y = s[w][i];
-      if (w < wave) before += y;
-      total += y;
+    uint32_t waves = 0, total = 0;
+    for (uint32_t w = 0; w < kThreads / kWave; ++w) {
+      const uint32_t y = s[w][i];
+      if (w < wave) waves = add_sat(waves, y);
+      total = add_sat(total, y);
     }
-    v[i] = before + x[i] - v[i];
+    v[i] = add_sat(waves, before[i]);
     all[i] = total;
   }
   __syncthreads();
@@ -94,20 +93,20 @@ __device__ __forceinline__ int32_t request_of(P start, uint32_t n, int32_t r) {
 // One workgroup, a thread per request (some in turn where there are more): new tokens' rows and
 // pages to give back and to take by prefix sums, and the ids given back to the stack.  What the
 // stack holds in the end decides who is served, so the pages given back are counted for all requests
-// first.  Sums in 64 bits: no lengths overflow them.  Where the step is small (kOne) the
-// same workgroup then writes the rows, from LDS.
+// first.  Where the step is small (kOne) the same workgroup then writes the rows, from LDS.
 //
 // Bound by its chain of loads and barriers (lengths, table entries, sums, stack, rows).
-template <bool kOne>
+template <bool kOne, uint32_t kThreads>
 __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step, ibp_kv_assigned out,
                                                         Share* __restrict__ shares) {
-  __shared__ uint64_t s_sum[kWaves][2];
+  constexpr uint32_t kWaves = kThreads / kWave;
+  __shared__ uint32_t s_sum[kWaves][2];
   __shared__ unsigned int s_unserved;
-  __shared__ unsigned long long s_taken;
+  __shared__ unsigned int s_taken;
   __shared__ Share s_share[kOne ? kThreads : 1];
   __shared__ int32_t s_start[kOne ? kThreads + 1 : 1];
   __shared__ Gift s_gift[kThreads];
-  __shared__ uint64_t s_at[kThreads];
+  __shared__ uint32_t s_at[kThreads];
   __shared__ unsigned int s_ended;
   const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const uint32_t turns = (step.n_seqs + kThreads - 1) / kThreads;
@@ -120,20 +119,20 @@ __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step
   // request t * kThreads + tid, from its lengths and the rows before it
   int32_t had, keep, held, wanted;
   int64_t want;
-  uint64_t rows[1], rows_all[1];
+  uint32_t rows[1], rows_all[1];
   bool fits;
-  auto look = [&](uint32_t t, uint64_t rows_before) {
+  auto look = [&](uint32_t t, uint32_t rows_before) {
     const uint32_t s = t * kThreads + tid;
     const bool have = s < step.n_seqs;
     had = have ? max(step.had[s], 0) : 0;
     keep = have && step.keep ? min(max(step.keep[s], 0), had) : had;
     const int32_t add = have ? max(step.add[s], 0) : 0;
     want = (int64_t)keep + add;
-    rows[0] = (uint64_t)add;
-    scan<1>(rows, rows_all, (uint64_t(*)[1])s_sum);
-    rows[0] += rows_before;
+    rows[0] = (uint32_t)add;
+    scan<1, kThreads>(rows, rows_all, s_sum);
+    rows[0] = add_sat(rows_before, rows[0]);
     fits = have && want <= (int64_t)IBP_KV_MAX_TOKENS && had <= (int32_t)IBP_KV_MAX_TOKENS &&
-           rows[0] + (uint64_t)add <= step.n_rows;
+           add_sat(rows[0], (uint32_t)add) <= step.n_rows;
     held = fits && had ? (int32_t)pool.page.div((uint32_t)had - 1) + 1 : 0;
     wanted = fits && want ? (int32_t)pool.page.div((uint32_t)want - 1) + 1 : 0;
     held = min(held, (int32_t)pool.max_pages);
@@ -149,9 +148,9 @@ __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step
 #pragma unroll
     for (int32_t j = 0; j < kFew; ++j) ids[j] = row[min(j, n - 1)];
   };
-  auto gives = [&](uint32_t t) -> uint64_t {
+  auto gives = [&](uint32_t t) -> uint32_t {
     const int32_t n = fits ? max(held - wanted, 0) : 0;
-    uint64_t some = 0;
+    uint32_t some = 0;
     if (tid == 0) s_ended = 0;
     __syncthreads();
     if (n > kFew) {
@@ -182,7 +181,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step
     return n > kFew ? s_at[tid] : some;
   };
   // the same entries to the stack, from place `at` on
-  auto give = [&](uint32_t t, uint64_t at) {
+  auto give = [&](uint32_t t, uint32_t at) {
+    at = min(at, 0x7FFFFFFFu);  // past the stack's end already: no sum with an entry's number passes 32 bits
     const int32_t n = fits ? max(held - wanted, 0) : 0;
     if (n > kFew) s_at[tid] = at;
     __syncthreads();
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step
     for (uint32_t e = wave; e < s_ended; e += kWaves) {
       const Gift g = s_gift[e];
       const int32_t* row = pool.table + (uint64_t)(t * kThreads + g.tid) * pool.table_stride + g.wanted;
-      uint64_t to = s_at[g.tid];
+      uint32_t to = s_at[g.tid];
       for (int32_t j = 0; j < g.n; j += kAtOnce) {
         int32_t ids[4];
 #pragma unroll
@@ -210,41 +210,41 @@ __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
           const uint64_t there = __ballot(is_page(pool, ids[a]));
-          const uint64_t mine = to + __builtin_popcountll(there & ((1ull << lane) - 1));
+          const uint32_t mine = to + (uint32_t)__builtin_popcountll(there & ((1ull << lane) - 1));
           if (is_page(pool, ids[a]) && mine < pool.n_pages) pool.free_pages[mine] = ids[a];
-          to += __builtin_popcountll(there);
+          to += (uint32_t)__builtin_popcountll(there);
         }
       }
     }
   };
 
-  uint64_t rows_before = 0, given = 0, mine = 0;
+  uint32_t rows_before = 0, given = 0, mine = 0;
   for (uint32_t t = 0; t < turns; ++t) {
     look(t, rows_before);
-    rows_before += rows_all[0];
+    rows_before = add_sat(rows_before, rows_all[0]);
     mine = gives(t);
-    uint64_t v[1] = {mine}, all[1];
     if (turns > 1) {
-      scan<1>(v, all, (uint64_t(*)[1])s_sum);
-      given += all[0];
+      uint32_t v[1] = {mine}, all[1];
+      scan<1, kThreads>(v, all, s_sum);
+      given = add_sat(given, all[0]);
     }
   }
-  uint64_t pages_before[2] = {0, 0};  // given back, taken
-  if (turns > 1) rows_before = 0;
-  const uint64_t rows_total = rows_before;
-  uint64_t avail = min(count0 + given, (uint64_t)pool.n_pages);
+  uint32_t pages_before[2] = {0, 0};  // given back, taken
+  const uint32_t rows_total = rows_before;
+  rows_before = 0;
+  uint32_t avail = min(add_sat(count0, given), pool.n_pages);
   for (uint32_t t = 0; t < turns; ++t) {
     const uint32_t s = t * kThreads + tid;
     if (turns > 1) {
       look(t, rows_before);
-      rows_before += rows_all[0];
+      rows_before = add_sat(rows_before, rows_all[0]);
       mine = gives(t);
     }
-    const uint64_t need = fits ? (uint64_t)max(wanted - held, 0) : 0;
-    uint64_t v[2] = {mine, need}, all[2];
-    scan<2>(v, all, s_sum);
-    if (turns == 1) avail = min(count0 + all[0], (uint64_t)pool.n_pages);
-    const uint64_t upto = pages_before[1] + v[1] + need;
+    const uint32_t need = fits ? (uint32_t)max(wanted - held, 0) : 0;
+    uint32_t v[2] = {mine, need}, all[2];
+    scan<2, kThreads>(v, all, s_sum);
+    if (turns == 1) avail = min(add_sat(count0, all[0]), pool.n_pages);
+    const uint32_t upto = add_sat(add_sat(pages_before[1], v[1]), need);
     const bool served = fits && (need == 0 || upto <= avail);
     if (s < step.n_seqs) {
       Share share;
@@ -253,21 +253,21 @@ __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step
       share.keep = served ? keep : -1;
       if (kOne) {
         s_share[tid] = share;
-        s_start[tid] = (int32_t)min(rows[0], (uint64_t)step.n_rows);
+        s_start[tid] = (int32_t)min(rows[0], step.n_rows);
       } else {
         shares[s] = share;
       }
-      out.q_start[s] = (int32_t)min(rows[0], (uint64_t)step.n_rows);
+      out.q_start[s] = (int32_t)min(rows[0], step.n_rows);
       out.kv_len[s] = served ? (int32_t)want : 0;
       out.length[s] = served ? (int32_t)want : had;
       if (!served) atomicAdd(&s_unserved, 1u);
-      else if (need) atomicMax(&s_taken, (unsigned long long)upto);
+      else if (need) atomicMax(&s_taken, upto);
     }
-    give(t, count0 + pages_before[0] + v[0]);
-    pages_before[0] += all[0];
-    pages_before[1] += all[1];
+    give(t, add_sat(add_sat(count0, pages_before[0]), v[0]));
+    pages_before[0] = add_sat(pages_before[0], all[0]);
+    pages_before[1] = add_sat(pages_before[1], all[1]);
   }
-  const int32_t end = (int32_t)min(turns > 1 ? rows_before : rows_total, (uint64_t)step.n_rows);
+  const int32_t end = (int32_t)min(rows_total, step.n_rows);
   __threadfence_block();
   __syncthreads();
   if (tid == 0) {
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(256) void k_kv_assign_rows(PagePool pool, Step step
   }
 }
 
-bool one_launch(uint32_t n_seqs, uint64_t n_rows) { return n_seqs <= kThreads && n_rows <= kOneRows; }
+bool one_launch(uint32_t n_seqs, uint64_t n_rows) { return n_seqs <= kMostThreads && n_rows <= kOneRows; }
 
 }  // namespace
 
@@ -323,10 +323,14 @@ uint64_t assign_workspace(uint32_t n_seqs, uint64_t n_rows) {
 hipError_t launch_assign(const PagePool& pool, const Step& step, const ibp_kv_assigned& out,
                          void* workspace, hipStream_t s) {
   if (one_launch(step.n_seqs, step.n_rows)) {
-    hipLaunchKernelGGL(k_kv_assign<true>, dim3(1), dim3(kThreads), 0, s, pool, step, out, nullptr);
+    if (step.n_seqs <= kFewThreads && step.n_rows <= 4 * kFewThreads)
+      hipLaunchKernelGGL((k_kv_assign<true, kFewThreads>), dim3(1), dim3(kFewThreads), 0, s, pool, step, out, nullptr);
+    else
+      hipLaunchKernelGGL((k_kv_assign<true, kMostThreads>), dim3(1), dim3(kMostThreads), 0, s, pool, step, out, nullptr);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(k_kv_assign<false>, dim3(1), dim3(kThreads), 0, s, pool, step, out, (Share*)workspace);
+  hipLaunchKernelGGL((k_kv_assign<false, kMostThreads>), dim3(1), dim3(kMostThreads), 0, s, pool, step, out,
+                     (Share*)workspace);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || step.n_rows == 0) return e;
   DeviceInfo di;
