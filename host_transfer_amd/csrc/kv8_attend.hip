@@ -41,10 +41,10 @@ hipError_t plan8(const Cache8& c, const Batch& b, uint32_t n_q_heads, Plan8* p) 
     if (shares > b.n_seqs * tiles) shares = b.n_seqs * tiles;
     if (shares > kMaxSplits) shares = kMaxSplits;
     p->shares = p->places = (uint32_t)shares;
-    p->wide_join = shares > 32 * (uint64_t)b.n_seqs && tiles > 32;
+    // (a launch's threads are counted in 32 bits)
+    p->wide_join = shares > 32 * (uint64_t)b.n_seqs && tiles > 32 && (uint64_t)b.n_rows * n_q_heads <= 0x3FFFFFull;
   }
-  if ((uint64_t)p->places * head_blocks > 0xFFFFFFull) return hipErrorInvalidConfiguration;
-  return p->wide_join && (uint64_t)b.n_rows * n_q_heads > 0x3FFFFFull ? hipErrorInvalidConfiguration : hipSuccess;
+  return (uint64_t)p->places * head_blocks > 0xFFFFFFull ? hipErrorInvalidConfiguration : hipSuccess;
 }
 
 constexpr uint64_t kHeadBytes = (uint64_t)kMaxShared * sizeof(int2);

@@ -438,11 +438,47 @@ def test_attend_ends_of_the_range(dtype, q_len, h):
             # least step, 2^-24, rounds by up to 2^-25: up to 2^-24 of the value, and of a mean of them
             ref[0], ref[2] = ref[0].clamp(-65504, 65504), ref[2] + 2.0 ** -24
         K.check_attention(c, out, lse, ref, f"e={e}")
+    if dtype is F16:  # past twice the type's range: infinities, of the rows that see them
+        c = K8.Case8([(q_len, 300), (q_len, 77)], dtype=dtype, d=64, h=h, group=2, page=16)
+        for s, (_, n) in enumerate(c.lens):
+            for j, code in ((0, 0x38), (n - 1, 0xB8), (n - 1 - q_len // 2, 0x38), (3, 0xB0)):
+                at = int(c.table[s, j // 16]), j % 16
+                c.ve[at[0]] = 144
+                c.v8.view(torch.uint8)[at[0]] &= 0x80  # (the block's others are zeros)
+                c.v8.view(torch.uint8)[at][..., j % 60] = code
+        c.renew()
+        c.v[c.v.abs() > 131000] *= math.inf  # 2^17; 2^16 is read as it is
+        log(f"past the range {dtype} q={q_len} h={h}")
+        for window in (0, 60):
+            out, lse = run_attend(c, 0.1, window=window)
+            K.check_attention(c, out, lse, K.attention(c, 0.1, window=window), "past the range")
     for scale in (0.0, -0.3, 5.0):
         c = K8.Case8([(q_len, 300), (q_len, 77)], dtype=dtype, d=64, h=h, group=2, page=16, strange=True)
         log(f"scale {scale}")
         out, lse = run_attend(c, scale)
         K.check_attention(c, out, lse, K.attention(c, scale), f"scale={scale}")
+
+
+@pytest.mark.parametrize("n_seqs,h,q_len", [(3, 4, 1), (64, 4, 2), (65, 1, 1), (200, 4, 1), (300, 1, 3), (1024, 1, 1),
+                                            (1030, 1, 1)])
+def test_attend_keys_shared_out(n_seqs, h, q_len):
+    """Sequences of very different lengths, some without rows or keys, whose keys are shared out over
+    workgroups: up to 64 sequences, more, and more than are shared out."""
+    rng = torch.Generator().manual_seed(n_seqs)
+    lens = []
+    for s in range(n_seqs):
+        r = int(torch.randint(0, 10, (1,), generator=rng))
+        kv = int(torch.randint(1, 120, (1,), generator=rng))
+        lens.append({0: (0, kv), 1: (min(q_len, 1), 0), 2: (q_len, q_len)}.get(r, (q_len, q_len + kv)))
+    lens[n_seqs // 2], lens[0] = (q_len, 1500), (1, 700)
+    c = K8.Case8(lens, dtype=BF16, h=h, group=2, d=16, page=16, strange=True, fill=math.nan, tail_rows=1, seed=n_seqs)
+    for causal, window, max_kv in ((True, 0, None), (True, 200, None), (False, 0, 30000)):
+        if max_kv:
+            wider_table(c, max_kv)
+        log(f"keys shared out: {n_seqs} sequences, h={h} q={q_len} causal={causal} window={window}")
+        out, lse = run_attend(c, 0.25, causal, window, max_kv=max_kv)
+        K.check_attention(c, out, lse, K.attention(c, 0.25, causal=causal, window=window), f"window={window}")
+        assert (out[c.n - 1:] == PAD).all() and (lse[c.n - 1:] == PAD).all()
 
 
 @pytest.mark.parametrize("q_len", [1, 2, 40])
