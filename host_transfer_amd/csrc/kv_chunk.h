@@ -276,6 +276,29 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       }
     }
   };
+  // a step's V and K, all pieces read before the first is converted (past the last tile: of what the stage
+  // holds, not used)
+  auto unpack_both = [&](uint16_t* to_v, uint32_t ve, uint16_t* to_k, uint32_t ke) {
+    if constexpr (kEight) {
+      const uint32_t first = wave * RPL8 + lane / CH8, c = lane % CH8 * 2;
+      uint4 codes[2 * ST8];
+      uint32_t ex[2 * ST8];
+#pragma unroll
+      for (int i = 0; i < 2 * ST8; ++i) {
+        codes[i] = s_code[(i < ST8 ? ST8 * kThreads : 0) + i % ST8 * kThreads + tid];
+        ex[i] = (uint32_t)__shfl((int)(i < ST8 ? ve : ke), (int)(first + i % ST8 * RPR8));
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * ST8; ++i) {
+        const uint32_t r = first + i % ST8 * RPR8;
+        uint16_t* to = (i < ST8 ? to_v : to_k) + r * DL;
+        const uint32_t sw = i < ST8 ? swizzle_v(r) : swizzle_k(r);
+        const float power = Read8<T>::power(ex[i]);
+        *(V8<T>*)(to + ((c ^ sw) << 3)) = Read8<T>::eight(codes[i].x, codes[i].y, power);
+        *(V8<T>*)(to + (((c + 1) ^ sw) << 3)) = Read8<T>::eight(codes[i].z, codes[i].w, power);
+      }
+    }
+  };
   auto bring = [&](const E* base, uint64_t at, uint64_t seen, uint32_t lds, bool is_k) {
     if constexpr (kEight) return bring8(base, at, seen, is_k);
     else {
@@ -507,10 +530,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       if (t0 + kKeys < end) bound(t0 + kKeys, seen1, nxt, fmaxf(most, most1));
     }
     wait_loads();
-    if (kEight) {
-      if (t0 + kKeys < end) unpack(s_v[buf ^ 1], ve1, false);
-      if (t0 + 2 * kKeys < end) unpack(s_k[buf], ke2, true);
-    }
+    if (kEight) unpack_both(s_v[buf ^ 1], ve1, s_k[buf], ke2);
     lds_barrier();
     at1 = at2;
     seen1 = seen2;
