@@ -95,7 +95,9 @@ __device__ __forceinline__ int32_t request_of(P start, uint32_t n, int32_t r) {
 // stack holds in the end decides who is served, so the pages given back are counted for all requests
 // first.  Where the step is small (kOne) the same workgroup then writes the rows, from LDS.
 //
-// Bound by its chain of loads and barriers (lengths, table entries, sums, stack, rows).
+// Bound by its chain of loads and barriers (lengths, table entries, sums, stack, rows): 20 requests of one
+// token 3.7 us, 250 with drafts, five of them ended, 8.2 (12.3 with sums through LDS in 64 bits), 64 with
+// 123,000 rows 7.2 and 4 for the rows (2 MB).  One workgroup: sums over several would need a launch each.
 template <bool kOne, uint32_t kThreads>
 __global__ __launch_bounds__(kThreads) void k_kv_assign(PagePool pool, Step step, ibp_kv_assigned out,
                                                         Share* __restrict__ shares) {
