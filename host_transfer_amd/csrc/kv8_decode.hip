@@ -1,7 +1,7 @@
 // kv8_decode.hip -- attention of few rows that share their keys over a cache in 8 bits: one new token
 // (or a few) of a sequence with the query heads of one key head.
-#include "ibp_device.h"
 #include "kv8_attend.h"
+#include "kv_wave.h"
 
 namespace ibp {
 namespace kv {

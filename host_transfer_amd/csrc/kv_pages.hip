@@ -1,6 +1,6 @@
 // kv_pages.hip -- a step's page tables, slots and positions from the requests' lengths.
-#include "ibp_device.h"
 #include "kv_pages.h"
+#include "kv_wave.h"
 
 namespace ibp {
 namespace kv {

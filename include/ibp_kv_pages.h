@@ -82,6 +82,7 @@ typedef struct {
  *   The stack and the lengths are what this call and its caller make them: a page
  *   that is on the stack twice, or there and in a row, is given to two requests.
  *   workspace   ibp_kv_assign_workspace() bytes, 16 B aligned (NULL if 0).
+ * Steps of one pool must follow each other: two at a time race.
  * Run again with the same `had`, `keep`, `add` and free_count (outputs elsewhere) it gives the same again.
  * Errors: NULL pointer; sizes; alignment; arrays that overlap (IBP_ERR_SIZE).
  */
