@@ -118,28 +118,33 @@ __device__ __forceinline__ float largest(const float (&x)[8], float most) {
 // registers between its maximum and their codes, further ones are formed again from
 // memory (L2).  The blocks are counted by sequence, up to seq_blocks each, or (seq_blocks 0), where
 // that would be more units than there are rows (a long prompt beside many single tokens), by
-// rows, of which the first of each block works.  Where the exponent rises, the tokens in front of the new ones are rounded to it.
+// rows, of which the first of each block works.  kHeads: few new tokens a block, many sequences: the lanes of
+// a wave hold HW heads' rows of one token, each head's exponent its own lanes' (227 single tokens of
+// 40 heads of 64 17.5 us without, 8.3 with).  Where the exponent rises, the tokens in front of the new ones are rounded to it.
 // The waves behind: queries, a wave (several, `parts`, for few rows) per row, as k_kv_append.
 // Bound by reading the 16-bit rows and writing them or half of them: 16,800 rows of 32 + 8 + 8 heads of 128
 // (387 MB) 88 us, 4.4 TB/s (155 with four kept turns, whose registers leave two waves a SIMD; 92 with
 // a launch each for keys and queries, 94 with the queries first, 89 with both in turn).  One token's call 5.4
 // us, its chain of lookups; the rows are requested ahead of it.
-template <typename T, int L>
+template <typename T, int L, bool kHeads>
 __global__ __launch_bounds__(256, 4) void k_kv8_append(Cache8 cache, Batch b, Rows k, Rows v, Rows q, Rows q_out,
                                                     Turning t, const T* __restrict__ q_norm,
                                                     const T* __restrict__ k_norm, uint32_t seq_blocks,
                                                     uint64_t kv_units, uint32_t parts) {
   constexpr uint32_t HW = kWave / L;  // rows of a wave at a time
+  constexpr uint32_t kStep = kHeads ? 1 : HW;  // tokens of a turn
   constexpr uint32_t kKeep = 2;
   typedef V8<T> v8;
   const uint32_t lane = threadIdx.x % kWave, c = lane % L, sub = lane / L;
   const Pieces p = pieces_of(t, c);
   uint64_t u = (uint64_t)blockIdx.x * kWaves + uniform(threadIdx.x / kWave);
   if (u < kv_units) {
-    const uint32_t hh = (uint32_t)(u % (2 * cache.n_heads));
-    u /= 2 * cache.n_heads;
-    const bool is_v = hh >= cache.n_heads;
-    const uint32_t h = is_v ? hh - cache.n_heads : hh;
+    const uint32_t side = kHeads ? (cache.n_heads + HW - 1) / HW : cache.n_heads;  // units of K, of V
+    const uint32_t hh = (uint32_t)(u % (2 * side));
+    u /= 2 * side;
+    const bool is_v = hh >= side;
+    const uint32_t h = (is_v ? hh - side : hh) * (kHeads ? HW : 1) + (kHeads ? sub : 0);
+    const uint32_t turn_at = kHeads ? 0 : sub;  // this lane's token of a turn
     const int32_t s = seq_blocks ? (int32_t)(u / seq_blocks) : seq_of_row(b, (int32_t)u);
     if (s < 0) return;
     const Seq sq = load_seq(b, (uint32_t)s);
@@ -169,7 +174,7 @@ __global__ __launch_bounds__(256, 4) void k_kv8_append(Cache8 cache, Batch b, Ro
     const Rows& src = is_v ? v : k;
     // token `at`, normed and rotated; false if it is not placed (its values are then zeros)
     auto row = [&](int32_t at, float (&x)[8], float (&y)[8]) -> bool {
-      bool on = at < end;
+      bool on = at < end && (!kHeads || h < cache.n_heads);
       const uint32_t r = (uint32_t)(sq.row0 + (at - sq.first));
       int64_t pos = 0;
       if (t.rope) {
@@ -196,10 +201,10 @@ __global__ __launch_bounds__(256, 4) void k_kv8_append(Cache8 cache, Batch b, Ro
     bool on[kKeep];
 #pragma unroll
     for (uint32_t i = 0; i < kKeep; ++i) {
-      on[i] = row(begin + (int32_t)(i * HW + sub), x[i], y[i]);
+      on[i] = row(begin + (int32_t)(i * kStep + turn_at), x[i], y[i]);
       most = largest(y[i], largest(x[i], most));
     }
-    if (!there) return;
+    if (!there || (kHeads && h >= cache.n_heads)) return;  // (whole heads leave: no lane that another asks)
     uint8_t* codes = (is_v ? cache.v : cache.k) + (uint64_t)(uint32_t)id * cache.page_stride +
                      (uint64_t)in * cache.token_stride + (uint64_t)h * cache.head_stride;
     uint8_t* exp = (is_v ? cache.v_exp : cache.k_exp) +
@@ -210,18 +215,19 @@ __global__ __launch_bounds__(256, 4) void k_kv8_append(Cache8 cache, Batch b, Ro
       if (p.has0) *(uint2*)(dst + p.c0 * 8) = encode8(x, inv);
       if (p.has1) *(uint2*)(dst + p.c1 * 8) = encode8(y, inv);
     };
-    for (int32_t at = begin + (int32_t)(kKeep * HW); at < end; at += HW) {
+    for (int32_t at = begin + (int32_t)(kKeep * kStep); at < end; at += kStep) {
       float xx[8], yy[8];
-      row(at + (int32_t)sub, xx, yy);
+      row(at + (int32_t)turn_at, xx, yy);
       most = largest(yy, largest(xx, most));
     }
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
+    for (int d = 1; d < (kHeads ? L : kWave); d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
     const uint32_t e = max(exponent_of(most), was);
     const float inv = __uint_as_float(e < 254 ? (254 - e) << 23 : 0x400000u);
     if (begin > base && e > was) {
       const float shift = e - was < 127 ? __uint_as_float((127 + was - e) << 23) : 0.f;
-      for (int32_t at = base + (int32_t)sub; at < begin; at += HW) {
+#pragma unroll 4
+      for (int32_t at = base + (int32_t)turn_at; at < begin; at += kStep) {
         uint8_t* dst = codes + (uint64_t)(uint32_t)(at - base) * cache.token_stride;
         float xx[8];
         if (p.has0) {
@@ -238,13 +244,13 @@ __global__ __launch_bounds__(256, 4) void k_kv8_append(Cache8 cache, Batch b, Ro
         }
       }
     }
-    if (lane == 0) *exp = (uint8_t)e;
+    if ((kHeads ? c : lane) == 0) *exp = (uint8_t)e;
 #pragma unroll
     for (uint32_t i = 0; i < kKeep; ++i)
-      if (on[i]) put(begin + (int32_t)(i * HW + sub), x[i], y[i], inv);
-    for (int32_t at = begin + (int32_t)(kKeep * HW); at < end; at += HW) {
+      if (on[i]) put(begin + (int32_t)(i * kStep + turn_at), x[i], y[i], inv);
+    for (int32_t at = begin + (int32_t)(kKeep * kStep); at < end; at += kStep) {
       float xx[8], yy[8];
-      if (row(at + (int32_t)sub, xx, yy)) put(at + (int32_t)sub, xx, yy, inv);
+      if (row(at + (int32_t)turn_at, xx, yy)) put(at + (int32_t)turn_at, xx, yy, inv);
     }
     return;
   }
@@ -315,7 +321,13 @@ hipError_t run_append8(const Cache8& c, const Batch& b, const Rows& k, const Row
     kv_units = b.n_rows;
     seq_blocks = 0;
   }
-  kv_units *= 2 * c.n_heads;
+  // Few new tokens a block leave most lanes of a wave per head idle: then a head to each of their groups, once
+  // there are more waves than the GPU holds (below, a block whose exponent rises is rounded anew faster
+  // with its tokens side by side).
+  constexpr uint32_t HW = kWave / L;
+  const bool by_heads = 2 * b.max_q <= HW && 2 * b.max_q <= c.n_heads &&
+                        kv_units * 2 * c.n_heads > (uint64_t)di.cus * 16;
+  kv_units *= 2 * (by_heads ? (c.n_heads + HW - 1) / HW : c.n_heads);
   // few rows: a row's queries over several waves, until every CU has eight
   const uint32_t turns = (q.n_heads * L + kWave - 1) / kWave;
   uint32_t parts = (uint32_t)(((uint64_t)di.cus * 8 + b.n_rows - 1) / b.n_rows);
@@ -324,9 +336,12 @@ hipError_t run_append8(const Cache8& c, const Batch& b, const Rows& k, const Row
   const uint64_t units = kv_units + (q.n_heads ? (uint64_t)b.n_rows * parts : 0);
   const uint64_t blocks = (units + kWaves - 1) / kWaves;
   if (blocks > 0xFFFFFFull) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((k_kv8_append<T, L>), dim3((uint32_t)blocks), dim3(256), 0, s, c, b, k, v, q, q_out, t,
-                     (const T*)q_norm, (const T*)k_norm, seq_blocks, kv_units, parts);
-  return hipGetLastError();
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks), dim3(256), 0, s, c, b, k, v, q, q_out, t, (const T*)q_norm,
+                       (const T*)k_norm, seq_blocks, kv_units, parts);
+    return hipGetLastError();
+  };
+  return by_heads ? launch(k_kv8_append<T, L, true>) : launch(k_kv8_append<T, L, false>);
 }
 
 }  // namespace

@@ -212,6 +212,43 @@ def test_append_long_prompt_beside_single_tokens():
         check_q(c, got[4], x[:, :3], placed, held, False, False)
 
 
+@pytest.mark.parametrize("dtype,d,h,q_len,block,page", [
+    (BF16, 64, 8, 1, 16, 16), (F16, 64, 20, 4, 8, 16), (BF16, 128, 8, 1, 16, 32), (F16, 128, 11, 3, 16, 16),
+    (BF16, 256, 4, 2, 32, 32), (F16, 80, 9, 2, 1, 4), (BF16, 128, 40, 4, 16, 16)])
+def test_append_few_tokens_of_many_sequences(dtype, d, h, q_len, block, page):
+    """Enough sequences of few new tokens that a wave holds several heads of a token: extended, fresh and
+    crossed blocks, exponents that rise and not, heads that are no multiple of a wave's."""
+    g = torch.Generator().manual_seed(d + h)
+    n = 300
+    lens = []
+    for s in range(n):
+        q = int(torch.randint(0, q_len + 1, (1,), generator=g))
+        lens.append((q, q + int(torch.randint(0, 40, (1,), generator=g))))
+    lens[7] = (q_len, q_len)
+    c = K8.Case8(lens, block=block, dtype=dtype, h=h, group=1, d=d, page=page, tail_rows=2, seed=h)
+    c.max_rows = c.most_kv = 1 << 30
+    c.table[11, 0] = -1
+    log(f"few tokens of many sequences {dtype} d={d} h={h} q={q_len} block={block}")
+    for rope, norm in ((0, False), (d if d % 32 == 0 else 48, True)):
+        scale = torch.exp2(torch.randint(-2, 3, (c.n, h + 3, 1), generator=g).float())
+        qkv = torch.randn((c.n, 3 + 2 * h, d), generator=g)
+        qkv[:, 3:3 + h] *= scale[:, 3:]
+        qkv[:, 3 + h:] *= scale[:, 3:]
+        qkv = qkv.to(dtype)
+        pos = torch.randint(0, 50, (c.n,), generator=g) if rope else None
+        table = K.rope_table(50, rope) if rope else None
+        if rope:
+            pos[5], pos[60] = -1, 50
+        kn = (1 + 0.3 * torch.randn(d, generator=g)).to(dtype) if norm else None
+        placed, held = placed_rows(c, pos, 50)
+        got = run_append(c, qkv, 3, rope=table, pos=pos, qn=kn, kn=kn)
+        safe = None if pos is None else pos.clamp(0, 49)
+        x = qkv.double()
+        new_k = K.norm_rotate(x[:, 3:3 + h], safe, table, False, kn, 1e-5)
+        check_cache(c, got, K8.append(c, new_k, x[:, 3 + h:], placed), (d + 48) * K.U32 if rope else 0.0)
+        check_q(c, got[4], K.norm_rotate(x[:, :3], safe, table, False, kn, 1e-5), placed, held, norm, rope)
+
+
 # ---------------------------------------------------------------- attention
 
 def run_attend(c, scale, causal=True, window=0, max_q=None, max_kv=None):
