@@ -15,6 +15,28 @@ struct Cache8 {
   FastDiv page, block;
 };
 
+constexpr uint32_t kMaxShared = 1024;  // items whose keys are shared out over workgroups
+constexpr uint32_t kLeastSteps = 8;    // of k_kv_chunk (64 keys each), that are worth a workgroup
+
+// How keys are shared out.  An item is a sequence (few rows: up to 32 that share a key head) or a tile of
+// kChunkRows of its rows: item (row_tiles - 1 - tile) * n_seqs + sequence.  A head group (one key head or four)
+// has `places` workgroups: one for each item (shares 0), or those that the items' keys are split over by
+// their lengths, which the kernel reads, at least one for each item and at most `shares` where that is enough.
+// A split item's results are in the workspace: heads[item] = (its first place, its splits), firsts[place] = (the
+// item that is split from there on, its splits; 0 elsewhere; many rows only), o
+// float[place][key head][row of the item][head_dim], ms float2[place][key head][row] of (base, sum).
+struct Plan8 {
+  uint32_t shares, places, rows, row_tiles, head_group;
+  bool wide_join;
+  int2 *heads, *firsts;
+  float* o;
+  float2* ms;
+};
+// A cache with its plan, as the chunk kernel takes it.
+struct Shared8 : Cache8 {
+  Plan8 plan;
+};
+
 hipError_t launch_append8(const Cache8& c, uint32_t dtype, const Batch& b, const Rows& k, const Rows& v,
                           const Rows& q, const Rows& q_out, const int64_t* positions, const float* rope,
                           uint64_t n_positions, uint32_t rope_dim, bool interleaved,

@@ -120,7 +120,8 @@ __device__ __forceinline__ float largest(const float (&x)[8], float most) {
 // that would be more units than there are rows (a long prompt beside many single tokens), by
 // rows, of which the first of each block works.  kHeads: few new tokens a block, many sequences: the lanes of
 // a wave hold HW heads' rows of one token, each head's exponent its own lanes' (227 single tokens of
-// 40 heads of 64 17.5 us without, 8.3 with).  Where the exponent rises, the tokens in front of the new ones are rounded to it.
+// 40 heads of 64 17.5 us without, 8.3 with).  Where the exponent rises, the tokens in front of the new ones
+// are rounded to it.
 // The waves behind: queries, a wave (several, `parts`, for few rows) per row, as k_kv_append.
 // Bound by reading the 16-bit rows and writing them or half of them: 16,800 rows of 32 + 8 + 8 heads of 128
 // (387 MB) 88 us, 4.4 TB/s (155 with four kept turns, whose registers leave two waves a SIMD; 92 with

@@ -8,21 +8,24 @@ namespace kv {
 namespace {
 
 template <typename T, int DP, bool kExact>
-hipError_t run_chunk8(const AttendPlan& p, const Cache8& c, const Batch& b, const Rows& q,
+hipError_t run_chunk8(const AttendPlan& p, const Shared8& c, const Batch& b, const Rows& q,
                       const Rows& out, float scale, uint32_t window, bool causal, float* lse,
-                      Partial part, hipStream_t s) {
-  hipLaunchKernelGGL((k_kv_chunk<T, DP, kExact, Cache8>), dim3((uint32_t)p.blocks), dim3(kThreads), 0, s, c,
-                     b, q, out, scale, window, causal, p.row_tiles, p.by_length, part, lse);
+                      hipStream_t s) {
+  hipLaunchKernelGGL((k_kv_chunk<T, DP, kExact, Shared8>), dim3((uint32_t)p.blocks), dim3(kThreads), 0, s, c,
+                     b, q, out, scale, window, causal, p.row_tiles, p.by_length, Partial{nullptr, nullptr, 1, 0}, lse);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_chunk8(const AttendPlan& p, const Cache8& c, uint32_t dtype, const Batch& b,
+hipError_t launch_chunk8(const AttendPlan& p, const Plan8& plan, const Cache8& c, uint32_t dtype, const Batch& b,
                          const Rows& q, const Rows& out, float scale, uint32_t window, bool causal,
-                         float* lse, Partial part, hipStream_t s) {
+                         float* lse, hipStream_t s) {
+  Shared8 cache;
+  (Cache8&)cache = c;
+  cache.plan = plan;
 #define IBP_KV8_CHUNK(T, DP, E) \
-  run_chunk8<T, DP, E>(p, c, b, q, out, scale, window, causal, lse, part, s)
+  run_chunk8<T, DP, E>(p, cache, b, q, out, scale, window, causal, lse, s)
 #define IBP_KV8_CHUNK_T(T)                                                                     \
   (c.head_dim == 64    ? IBP_KV8_CHUNK(T, 64, true)                                            \
    : c.head_dim < 64   ? IBP_KV8_CHUNK(T, 64, false)                                           \

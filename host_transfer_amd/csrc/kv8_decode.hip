@@ -1,7 +1,7 @@
 // kv8_decode.hip -- attention of few rows that share their keys over a cache in 8 bits: one new token
 // (or a few) of a sequence with the query heads of one key head.
 #include "kv8_attend.h"
-#include "kv_wave.h"
+#include "kv8_share.h"
 
 namespace ibp {
 namespace kv {
@@ -10,10 +10,11 @@ namespace {
 
 constexpr int kTile = 32;   // keys of a wave's step
 constexpr int kWaves = 4;
+constexpr uint32_t kManyRows = 8192;  // as the GPU holds waves
 
 // As k_kv_decode: a workgroup per (up to 16 NC rows that share a key head, split of their keys; all rows of
-// a sequence), its four waves over four key heads of the same tokens or over one head's keys in turn, each with a running maximum
-// and sum of its own.  A wave reads 32 keys' codes of K and of V at a time, neighbouring lanes
+// a sequence), its four waves over four key heads of the same tokens or over one head's keys in turn, each with a
+// running maximum and sum of its own.  A wave reads 32 keys' codes of K and of V at a time, neighbouring lanes
 // neighbouring pieces of 16 codes, makes 16-bit rows of them in its registers (two codes an instruction,
 // which applies the block's power of two too) and passes those through its own part of LDS, K first,
 // then V in its place: the first product reads rows, the second one transposed.
@@ -26,52 +27,6 @@ constexpr int kWaves = 4;
 // key heads (806 MB) 151 to 156 us, 5.2 to 5.3 TB/s, as a large copy runs; 24 sequences of 5 tokens over 1,638 to
 // 8,192 tokens (244 MB, two columns) 68 us.  Four workgroups a CU with one column (two 99 and 173 us for the
 // first two; three, each with its next tile on the way, 95 and 168).
-// The sequence and split of workgroup `place` of its head group, and the split's length: with n_s =
-// max(ceil(tiles_s / size), 1) workgroups for a sequence that has rows, size the least length with which
-// all sequences' are at most `shares`; sequences in their order.  s < 0: there is none for it.
-//   mine    2 * tiles + 1 of sequence `lane`, 0 where it has no rows; others', past 64, in `tiles`
-struct Part8 {
-  int32_t s, split, splits, size, place;  // place: the sequence's first workgroup
-};
-__device__ __forceinline__ Part8 part_of(uint32_t mine, const uint32_t* tiles, uint32_t n_seqs, uint32_t shares,
-                                         uint32_t place, uint32_t lane) {
-  auto at = [&](uint32_t j0) -> uint32_t { return j0 == 0 ? mine : j0 + lane < n_seqs ? tiles[j0 + lane] : 0; };
-  uint32_t total = 0, most = 0, active = 0;
-  for (uint32_t j0 = 0; j0 < n_seqs; j0 += kWave) {
-    const uint32_t t = at(j0);
-    total += wave_sum(t >> 1);
-    most = max(most, wave_max(t >> 1));
-    active += (uint32_t)__builtin_popcountll(__ballot(t & 1u));
-  }
-  // lo may be too short, hi is not: sum of ceil(t / hi) <= total / hi + active
-  uint32_t lo = max((total + shares - 1) / shares, 1u), hi = max(most, 1u);
-  if (shares > active) hi = min(hi, (total + shares - active - 1) / (shares - active));
-  hi = max(hi, lo);
-  auto splits = [&](uint32_t t, uint32_t size) { return t ? max(((t >> 1) + size - 1) / size, 1u) : 0u; };
-  while (lo < hi) {
-    const uint32_t mid = (lo + hi) / 2;
-    uint32_t n = 0;
-    for (uint32_t j0 = 0; j0 < n_seqs; j0 += kWave) n += wave_sum(splits(at(j0), mid));
-    if (n <= shares) hi = mid;
-    else lo = mid + 1;
-  }
-  Part8 p = {-1, 0, 0, (int32_t)hi, 0};
-  uint32_t before = 0;
-  for (uint32_t j0 = 0; j0 < n_seqs && p.s < 0; j0 += kWave) {
-    const uint32_t n = splits(at(j0), hi), upto = before + wave_prefix_sum(n);
-    const uint64_t here = __ballot(n && place >= upto - n && place < upto);
-    if (here) {
-      const uint32_t l = (uint32_t)__builtin_ctzll(here);
-      p.s = (int32_t)(j0 + l);
-      p.splits = (int32_t)lane_u32(n, l);
-      p.place = (int32_t)(lane_u32(upto, l) - lane_u32(n, l));
-      p.split = (int32_t)place - p.place;
-    }
-    before = lane_u32(upto, kWave - 1);
-  }
-  return p;
-}
-
 template <typename T, int DP, int kHeads, int NC>  // NC: columns of 16 rows
 __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
     Cache8 cache, Batch b, Rows q, Rows out, float scale_log2, uint32_t window, bool causal,
@@ -108,7 +63,7 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
     const int32_t from = first_lo(sq) / kBlockKeys * kBlockKeys;
     return max(last_hi(sq) - from + kBlockKeys - 1, 0) / kBlockKeys;
   };
-  Part8 at_ = {(int32_t)place, 0, 1, 0x7FFFFFFF, 0};
+  Part8 at_ = {(int32_t)place, 0, 1, 0};
   Seq sq;
   if (plan.shares) {
     // sequences past the first 64: their lengths where the rows of V will lie
@@ -148,7 +103,7 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
   // the split's keys, whole tiles of the workgroup
   const int32_t from = lo_a / kBlockKeys * kBlockKeys;
   const int32_t tiles = tiles_of(sq);
-  const int32_t per = min(at_.size, tiles);
+  const int32_t per = part_tiles(at_, tiles);
   const int32_t begin = from + min(at_.split * per, tiles) * kBlockKeys;
   const int32_t end = min(from + min((at_.split + 1) * per, tiles) * kBlockKeys, hi_e);
 
@@ -475,23 +430,32 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
   }
 }
 
-// A split row's place in the workspace: its first partial result, how many there are and how far apart;
-// n <= 1: the row is whole, or no sequence's.
+// What a place of the joins' grids has to join: `rows` rows from m0 of the item's, `n` results each (n <= 1: none).
 struct Parts8 {
-  uint64_t slot, step;
-  uint32_t n;
+  Seq sq;
+  uint32_t m0, rows, n, first;  // first: the place of the first result
 };
-__device__ __forceinline__ Parts8 parts_of(const Batch& b, const Rows& out, const Plan8& plan, uint32_t n_heads,
-                                           uint32_t row, uint32_t head) {
-  const int32_t s = seq_of_row(b, (int32_t)row);
-  if (s < 0) return Parts8{0, 0, 0};
-  const int2 of = plan.heads[s];
-  const uint32_t group = out.n_heads / n_heads;
-  const uint32_t i = row - (uint32_t)load_seq(b, (uint32_t)s).row0;
-  Parts8 p;
-  p.n = (uint32_t)of.y;
-  p.step = (uint64_t)n_heads * plan.rows;
-  p.slot = (uint64_t)of.x * p.step + (uint64_t)(head / group) * plan.rows + i * group + head % group;
+__device__ __forceinline__ Parts8 parts_of(const Batch& b, const Plan8& plan, uint32_t group, uint32_t u) {
+  Parts8 p = {};
+  int2 of;  // (of no meaning where the item has no rows)
+  uint32_t item = u;
+  p.first = u;
+  if (plan.row_tiles == 1) {
+    if (item >= b.n_seqs) return p;
+    of = plan.heads[item];
+    p.first = (uint32_t)of.x;
+  } else {  // (of the tiles of the longest sequence's rows most may have none)
+    if (u >= plan.places) return p;
+    of = plan.firsts[u];
+    if (of.y <= 1) return p;
+    item = (uint32_t)of.x;
+  }
+  p.sq = load_seq(b, item % b.n_seqs);
+  const uint32_t n_m = (uint32_t)max(p.sq.q_len, 0) * group;
+  p.m0 = (plan.row_tiles - 1 - item / b.n_seqs) * plan.rows;
+  if (p.m0 >= n_m) return p;
+  p.rows = min(plan.rows, n_m - p.m0);
+  if ((uint64_t)p.first + (uint32_t)of.y <= plan.places) p.n = (uint32_t)of.y;  // (else: overlapping sequences)
   return p;
 }
 template <typename T>
@@ -509,50 +473,100 @@ __device__ __forceinline__ void finish(const Rows& out, uint32_t row, uint32_t h
     lse[(uint64_t)row * out.n_heads + head] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
 }
 
-// The splits of a row together, a wave per (row, head): 64 splits' factors in its lanes, then `lanes` lanes
-// (four channels each) a split.  3,840 rows and heads of about 10 splits 12 us with a workgroup each.
-template <typename T>
+// The splits of rows together: a wave to one row of an item and key head, 64 splits' factors in its lanes, then
+// `lanes` lanes (four channels each) a split; or, where rows are many (kMany), to four rows for each
+// `lanes` lanes, so that what a wave looks up first serves them all (2 splits of 32,768 rows 12 us).  The
+// first turns' results are asked for beside the factors: 800 rows of about 6 splits 4.3 us (5.3 in turn).
+template <typename T, bool kMany>
 __global__ __launch_bounds__(256) void k_kv8_join(Batch b, Rows out, Plan8 plan, uint32_t n_heads,
                                                   uint32_t head_dim, uint32_t lanes, float* __restrict__ lse) {
-  const uint32_t lane = threadIdx.x % kWave;
-  const uint64_t unit = (uint64_t)blockIdx.x * 4 + uniform(threadIdx.x / kWave);
-  if (unit >= (uint64_t)b.n_rows * out.n_heads) return;
-  const uint32_t row = (uint32_t)(unit / out.n_heads), head = (uint32_t)(unit % out.n_heads);
-  const Parts8 p = parts_of(b, out, plan, n_heads, row, head);
-  if (p.n <= 1) return;
-  float mm = -INFINITY;
-  for (uint32_t e = lane; e < p.n; e += kWave) mm = fmaxf(mm, plan.ms[p.slot + e * p.step].x);
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
-  const float base = mm == -INFINITY ? 0.f : mm;
-  const uint32_t c = lane % lanes * 4, sub = lane / lanes, at_once = kWave / lanes;
+  const uint32_t lane = threadIdx.x % kWave, at_once = kWave / lanes;
+  const uint32_t n_r = kMany ? 4 * at_once : 1, parts = (plan.rows + n_r - 1) / n_r;  // rows of a wave
+  uint32_t u = blockIdx.x * 4 + uniform(threadIdx.x / kWave);
+  const uint32_t r0 = u % parts * n_r;
+  u /= parts;
+  const uint32_t kh = u % n_heads;
+  u /= n_heads;
+  const uint32_t group = out.n_heads / n_heads;
+  const Parts8 p = parts_of(b, plan, group, u);
+  const uint32_t n = p.n;
+  if (n <= 1 || r0 >= p.rows) return;
+  const uint32_t rows = min(n_r, p.rows - r0);
+  const uint64_t step = (uint64_t)n_heads * plan.rows, slot = p.first * step + (uint64_t)kh * plan.rows + r0;
+  const uint32_t c = lane % lanes * 4, sub = lane / lanes;
   const bool live = c < head_dim;
-  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  // a turn: four rows' parts of one split, or one row's of at_once splits
+  constexpr int kR = kMany ? 4 : 1;
+  constexpr uint32_t kAhead = kMany ? 2 : 4;
+  auto split_of = [&](uint32_t t) { return kMany ? t : t * at_once + sub; };
+  auto row_of = [&](int j) { return kMany ? sub * kR + j : 0; };
+  auto part = [&](uint32_t e, int j) -> f32x4 {
+    const uint64_t at = slot + min(row_of(j), rows - 1) + min(e, n - 1) * step;
+    return live ? *(const f32x4*)(plan.o + at * head_dim + c) : f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+  // factors: lane `lane` has row lane % n_r of split (lane / n_r) of every kWave / n_r; the first turns'
+  // results are on their way beside them
+  const uint32_t fr = lane % n_r, fe = lane / n_r, f_step = kWave / n_r;
+  const float2* ms = plan.ms + slot + min(fr, rows - 1);
+  const float2 nothing = make_float2(-INFINITY, 0.f);
+  float2 x = fe < n ? ms[fe * step] : nothing;
+  f32x4 ahead[kAhead][kR];
+#pragma unroll
+  for (uint32_t t = 0; t < kAhead; ++t)
+#pragma unroll
+    for (int j = 0; j < kR; ++j) ahead[t][j] = part(split_of(t), j);
+  float mm = x.x;
+  for (uint32_t e = fe + f_step; e < n; e += f_step) mm = fmaxf(mm, ms[e * step].x);
+  for (uint32_t d = n_r; d < (uint32_t)kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, (int)d));
+  const float base = mm == -INFINITY ? 0.f : mm;
+  f32x4 o[kR];
+#pragma unroll
+  for (int j = 0; j < kR; ++j) o[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   float z = 0.f;
-  for (uint32_t e0 = 0; e0 < p.n; e0 += kWave) {
-    const float2 x = e0 + lane < p.n ? plan.ms[p.slot + (e0 + lane) * p.step] : make_float2(-INFINITY, 0.f);
+  for (uint32_t e0 = 0; e0 < n; e0 += f_step) {
+    if (e0) x = e0 + fe < n ? ms[(e0 + fe) * step] : nothing;
     const float f = exp2_raw(x.x - base);
     z += f * x.y;
-    const uint32_t n = min(p.n - e0, (uint32_t)kWave);
-#pragma unroll 4
-    for (uint32_t e = 0; e < n; e += at_once) {
-      const float fe = __shfl(f, (int)min(e + sub, (uint32_t)kWave - 1));
-      if (!live || e + sub >= n) continue;
-      const f32x4 y = *(const f32x4*)(plan.o + (p.slot + (e0 + e + sub) * p.step) * head_dim + c);
+    const uint32_t some = min(n - e0, f_step);
+    auto add = [&](uint32_t t, int j, const f32x4& y) {
+      const uint32_t e = split_of(t);
+      const float fj = __shfl(f, (int)min(e * n_r + row_of(j), (uint32_t)kWave - 1));
+      if (e >= some) return;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] += scaled(y[r], fe);
+      for (int i = 0; i < 4; ++i) o[j][i] += scaled(y[i], fj);
+    };
+    const uint32_t turns = kMany ? some : (some + at_once - 1) / at_once;
+    for (uint32_t t0 = 0; t0 < turns; t0 += kAhead) {
+#pragma unroll
+      for (uint32_t t = 0; t < kAhead; ++t)
+#pragma unroll
+        for (int j = 0; j < kR; ++j) add(t0 + t, j, ahead[t][j]);
+      const bool last = t0 + kAhead >= turns;
+      if (last && e0 + f_step >= n) break;
+      const uint32_t next = last ? e0 + f_step : e0, nt = last ? 0 : t0 + kAhead;
+#pragma unroll
+      for (uint32_t t = 0; t < kAhead; ++t)
+#pragma unroll
+        for (int j = 0; j < kR; ++j) ahead[t][j] = part(next + split_of(nt + t), j);
     }
   }
+  for (uint32_t d = n_r; d < (uint32_t)kWave; d <<= 1) z += __shfl_xor(z, (int)d);
+  if (!kMany)
+    for (uint32_t d = lanes; d < (uint32_t)kWave; d <<= 1)
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) z += __shfl_xor(z, d);
-  for (uint32_t d = lanes; d < (uint32_t)kWave; d <<= 1)
+      for (int i = 0; i < 4; ++i) o[0][i] += __shfl_xor(o[0][i], (int)d);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[r] += __shfl_xor(o[r], (int)d);
-  finish<T>(out, row, head, c, live && sub == 0, o, z, mm, sub == 0 ? lse : nullptr);
+  for (int j = 0; j < kR; ++j) {
+    const uint32_t r = row_of(j), m = p.m0 + r0 + r;
+    const float zj = kMany ? __shfl(z, (int)r) : z, mj = kMany ? __shfl(mm, (int)r) : mm;
+    const bool mine = kMany ? r < rows : sub == 0;
+    finish<T>(out, (uint32_t)p.sq.row0 + m / group, kh * group + m % group, c, live && mine, o[j], zj, mj,
+              mine ? lse : nullptr);
+  }
 }
 
-// The same with a workgroup of 1024 for each (row, head), where the splits are many (128 rows and heads of 128
-// splits 8 us).
+// The same with a workgroup of 1024 for each (row, head), where the splits are many and the rows few (128 rows and
+// heads of 128 splits 8 us; 784 of 36 take 11 here, 7 with a wave each).
 template <typename T>
 __global__ __launch_bounds__(1024) void k_kv8_join_many(Batch b, Rows out, Plan8 plan, uint32_t n_heads,
                                                        uint32_t head_dim, uint32_t lanes,
@@ -563,10 +577,11 @@ __global__ __launch_bounds__(1024) void k_kv8_join_many(Batch b, Rows out, Plan8
   __shared__ float s_red[NW];
   __shared__ f32x4 s_o[kThreads];
   const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const uint32_t row = blockIdx.x / out.n_heads, head = blockIdx.x % out.n_heads;
-  const Parts8 p = parts_of(b, out, plan, n_heads, row, head);
-  if (p.n <= 1) return;
-  const float2 x = tid < p.n ? plan.ms[p.slot + tid * p.step] : make_float2(-INFINITY, 0.f);
+  const uint32_t r = blockIdx.x % plan.rows, kh = blockIdx.x / plan.rows % n_heads, group = out.n_heads / n_heads;
+  const Parts8 p = parts_of(b, plan, group, blockIdx.x / plan.rows / n_heads);
+  if (p.n <= 1 || r >= p.rows) return;
+  const uint64_t step = (uint64_t)n_heads * plan.rows, slot = p.first * step + (uint64_t)kh * plan.rows + r;
+  const float2 x = tid < p.n ? plan.ms[slot + tid * step] : make_float2(-INFINITY, 0.f);
   float mm = x.x;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) mm = fmaxf(mm, __shfl_xor(mm, d, kWave));
@@ -589,7 +604,7 @@ __global__ __launch_bounds__(1024) void k_kv8_join_many(Batch b, Rows out, Plan8
   if (live) {
 #pragma unroll 4
     for (uint32_t e = tid / lanes; e < p.n; e += at_once) {
-      const f32x4 y = *(const f32x4*)(plan.o + (p.slot + e * p.step) * head_dim + c);
+      const f32x4 y = *(const f32x4*)(plan.o + (slot + e * step) * head_dim + c);
 #pragma unroll
       for (int r = 0; r < 4; ++r) o[r] += scaled(y[r], s_f[e]);
     }
@@ -605,7 +620,27 @@ __global__ __launch_bounds__(1024) void k_kv8_join_many(Batch b, Rows out, Plan8
     }
     __syncthreads();
   }
-  if (tid < lanes) finish<T>(out, row, head, c, live, o, z, mm, lse);
+  const uint32_t m = p.m0 + r;
+  if (tid < lanes) finish<T>(out, (uint32_t)p.sq.row0 + m / group, kh * group + m % group, c, live, o, z, mm, lse);
+}
+
+template <typename T>
+hipError_t run_join8(const Plan8& p, const Cache8& c, const Batch& b, const Rows& out, float* lse, hipStream_t s) {
+  const uint32_t lanes = c.head_dim <= 64 ? 16 : c.head_dim <= 128 ? 32 : 64;
+  const uint64_t head_units = (uint64_t)(p.row_tiles == 1 ? b.n_seqs : p.places) * c.n_heads;
+  if (p.wide_join) {
+    hipLaunchKernelGGL(k_kv8_join_many<T>, dim3((uint32_t)(head_units * p.rows)), dim3(1024), 0, s, b, out, p,
+                       c.n_heads, c.head_dim, lanes, lse);
+    return hipGetLastError();
+  }
+  const bool many = (uint64_t)b.n_rows * out.n_heads >= kManyRows || p.row_tiles > 1;
+  const uint32_t n_r = many ? 4 * kWave / lanes : 1;
+  const dim3 grid((uint32_t)((head_units * ((p.rows + n_r - 1) / n_r) + 3) / 4));
+  if (many)
+    hipLaunchKernelGGL((k_kv8_join<T, true>), grid, dim3(256), 0, s, b, out, p, c.n_heads, c.head_dim, lanes, lse);
+  else
+    hipLaunchKernelGGL((k_kv8_join<T, false>), grid, dim3(256), 0, s, b, out, p, c.n_heads, c.head_dim, lanes, lse);
+  return hipGetLastError();
 }
 
 template <typename T, int DP, int kHeads, int NC>
@@ -614,18 +649,15 @@ hipError_t run_decode8(const Plan8& p, const Cache8& c, const Batch& b, const Ro
   hipLaunchKernelGGL((k_kv8_decode<T, DP, kHeads, NC>), dim3(p.places * (c.n_heads / kHeads)), dim3(256), 0, s,
                      c, b, q, out, scale * kLog2e * Read8<T>::kScale, window, causal, p, lse);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.shares == 0) return e;
-  const uint32_t lanes = c.head_dim <= 64 ? 16 : c.head_dim <= 128 ? 32 : 64;
-  const uint32_t units = b.n_rows * q.n_heads;
-  if (p.wide_join)
-    hipLaunchKernelGGL(k_kv8_join_many<T>, dim3(units), dim3(1024), 0, s, b, out, p, c.n_heads, c.head_dim, lanes, lse);
-  else
-    hipLaunchKernelGGL(k_kv8_join<T>, dim3((units + 3) / 4), dim3(256), 0, s, b, out, p, c.n_heads, c.head_dim, lanes,
-                       lse);
-  return hipGetLastError();
+  return e != hipSuccess || p.shares == 0 ? e : run_join8<T>(p, c, b, out, lse, s);
 }
 
 }  // namespace
+
+hipError_t launch_join8(const Plan8& p, const Cache8& c, uint32_t dtype, const Batch& b, const Rows& out, float* lse,
+                        hipStream_t s) {
+  return dtype == IBP_KV_F16 ? run_join8<_Float16>(p, c, b, out, lse, s) : run_join8<__bf16>(p, c, b, out, lse, s);
+}
 
 hipError_t launch_decode8(const Plan8& p, const Cache8& c, uint32_t dtype, const Batch& b, const Rows& q,
                           const Rows& out, float scale, uint32_t window, bool causal, float* lse,

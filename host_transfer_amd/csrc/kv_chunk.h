@@ -7,6 +7,7 @@
 
 #include "ibp_device.h"
 #include "kv8.h"
+#include "kv8_share.h"
 
 namespace ibp {
 namespace kv {
@@ -92,7 +93,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   constexpr int RPL = kWave / CH;                        // rows of a load
   constexpr int RPR = kThreads / CH;                     // rows of the four waves' loads
   constexpr int TILE = kKeys * DL;
-  constexpr bool kEight = __is_same(C, Cache8);
+  constexpr bool kEight = __is_same(C, Shared8);
   typedef std::conditional_t<kEight, In8<T>, T> W;  // what the weights' range goes by
   constexpr int CH8 = DL / 16, ST8 = kKeys * CH8 / kThreads;  // the same of codes: 16 to a piece
   constexpr int RPL8 = kWave / CH8, RPR8 = kThreads / CH8;
@@ -112,11 +113,56 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   uint32_t u = blockIdx.x;
   const uint32_t kh = u % cache.n_heads;
   u /= cache.n_heads;
-  const uint32_t split = u % part.splits;
-  u /= part.splits;
+  uint32_t split = 0;
+  if constexpr (!kEight) {
+    split = u % part.splits;
+    u /= part.splits;
+  }
+  const int32_t w = (int32_t)window;
+  auto pos_in = [&](const Seq& x, uint32_t m) { return max(x.first + (int32_t)(m / group), -1); };
+  auto lo_of = [&](int32_t pos) { return w ? max(pos - w + 1, 0) : 0; };
+  auto hi_in = [&](const Seq& x, int32_t pos) { return causal ? min(pos + 1, x.n_keys) : x.n_keys; };
   uint32_t s, tile;
   Seq sq;
-  if (!by_length) {
+  Part8 at_ = {0, 0, 1, 0};
+  bool shared = false;
+  if constexpr (kEight) shared = cache.plan.shares != 0;
+  if (shared) {
+    if constexpr (kEight) {
+      const Plan8& plan = cache.plan;
+      const uint32_t items = plan.row_tiles * b.n_seqs, place = u;
+      static_assert(kMaxShared * 4 <= sizeof(s_code), "the lengths fit");
+      uint32_t* s_tiles = (uint32_t*)s_code;
+      auto length = [&](uint32_t item, const Seq& x) -> uint32_t {
+        const uint32_t a = (row_tiles - 1 - item / b.n_seqs) * kRows, n = (uint32_t)max(x.q_len, 0) * group;
+        if (a >= n) return 0;
+        const int32_t from = lo_of(pos_in(x, a)) / kKeys * kKeys, to = hi_in(x, pos_in(x, min(a + kRows, n) - 1));
+        return (uint32_t)(max(to - from + kKeys - 1, 0) / kKeys) << 1 | 1u;
+      };
+      Seq mine = {0, 0, 0, 0};
+      if (lane < items) mine = load_seq(b, lane % b.n_seqs);
+      if (items > (uint32_t)kWave) {
+        for (uint32_t j = kWave + tid; j < items; j += kThreads) s_tiles[j] = length(j, load_seq(b, j % b.n_seqs));
+        __syncthreads();
+      }
+      at_ = part_of(length(lane, mine), s_tiles, items, plan.shares, place, lane, kLeastSteps);
+      if (items > (uint32_t)kWave) __syncthreads();
+      if (kh == 0 && tid == 0) {
+        const bool first = at_.s >= 0 && at_.split == 0;
+        if (first) plan.heads[at_.s] = make_int2(at_.place, at_.splits);
+        plan.firsts[place] = first ? make_int2(at_.s, at_.splits) : make_int2(0, 0);
+      }
+      if (at_.s < 0) return;
+      s = (uint32_t)at_.s % b.n_seqs;
+      tile = row_tiles - 1 - (uint32_t)at_.s / b.n_seqs;
+      const uint32_t l = (uint32_t)at_.s;
+      if (l < (uint32_t)kWave)
+        sq = Seq{(int32_t)lane_u32((uint32_t)mine.row0, l), (int32_t)lane_u32((uint32_t)mine.q_len, l),
+                 (int32_t)lane_u32((uint32_t)mine.first, l), (int32_t)lane_u32((uint32_t)mine.n_keys, l)};
+      else
+        sq = load_seq(b, s);
+    }
+  } else if (!by_length) {
     s = u % b.n_seqs;
     tile = row_tiles - 1 - u / b.n_seqs;
     sq = load_seq(b, s);
@@ -146,10 +192,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   const uint32_t m1 = min(m0 + kRows, n_m);
 
   // keys seen by rows m of the block or of a wave: [lo, hi) of the first and of the last
-  const int32_t w = (int32_t)window;
-  auto pos_of = [&](uint32_t m) { return max(sq.first + (int32_t)(m / group), -1); };
-  auto lo_of = [&](int32_t pos) { return w ? max(pos - w + 1, 0) : 0; };
-  auto hi_of = [&](int32_t pos) { return causal ? min(pos + 1, sq.n_keys) : sq.n_keys; };
+  auto pos_of = [&](uint32_t m) { return pos_in(sq, m); };
+  auto hi_of = [&](int32_t pos) { return hi_in(sq, pos); };
   const int32_t blk_lo = lo_of(pos_of(m0)), blk_hi = hi_of(pos_of(m1 - 1));
   const int32_t edge_lo = lo_of(pos_of(m1 - 1)), edge_hi = hi_of(pos_of(m0));
   const bool active = m0 + wave * 32 < m1;
@@ -162,7 +206,12 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
 
   const int32_t from = blk_lo / kKeys * kKeys;
   const int32_t tiles = max(blk_hi - from + kKeys - 1, 0) / kKeys;
-  const int32_t per = (tiles + (int32_t)part.splits - 1) / (int32_t)part.splits;
+  int32_t per = tiles;  // steps of a split
+  if constexpr (kEight) {
+    if (shared) per = part_tiles(at_, tiles), split = (uint32_t)at_.split;
+  } else {
+    per = (tiles + (int32_t)part.splits - 1) / (int32_t)part.splits;
+  }
   const int32_t begin = from + min((int32_t)split * per, tiles) * kKeys;
   const int32_t end = from + min(((int32_t)split + 1) * per, tiles) * kKeys;
   // a step with keys that some rows of the block see and others do not
@@ -616,8 +665,19 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       for (int r = 0; r < 16; ++r) o[t][r] *= Read8<T>::kScale;
   z = sum_half(z);
   const uint64_t unit = (uint64_t)row * q.n_heads + head;
-  if (part.splits > 1) {
-    float* to = part.row(unit, split);
+  bool whole = part.splits <= 1;
+  if constexpr (kEight) whole = at_.splits <= 1;
+  if (!whole) {
+    float *to;
+    float2* ms;
+    if constexpr (kEight) {
+      const uint64_t slot = ((uint64_t)u * cache.n_heads + kh) * cache.plan.rows + (m - m0);
+      to = cache.plan.o + slot * hd;
+      ms = cache.plan.ms + slot;
+    } else {
+      to = part.row(unit, split);
+      ms = part.ms + unit * part.splits + split;
+    }
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -626,7 +686,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
         if (c < hd)
           *(f32x4*)(to + c) = f32x4{o[t][4 * r], o[t][4 * r + 1], o[t][4 * r + 2], o[t][4 * r + 3]};
       }
-    if (half == 0) part.ms[unit * part.splits + split] = make_float2(top, z);
+    if (half == 0) *ms = make_float2(top, z);
     return;
   }
   const float inv = z == 0.f ? 0.f : 1.f / z;

@@ -350,7 +350,8 @@ def test_attend_single_tokens(dtype, d, h, group, page, block):
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("q_len,d,h,group,page", [
     (2, 128, 2, 8, 16), (3, 64, 4, 8, 16), (5, 128, 8, 4, 16), (4, 96, 1, 8, 24), (9, 192, 4, 3, 16), (6, 256, 1, 5, 64),
-    (17, 128, 4, 1, 16), (32, 64, 1, 1, 16), (33, 128, 2, 1, 16), (11, 128, 4, 3, 32)])
+    (17, 128, 4, 1, 16), (32, 64, 1, 1, 16), (33, 128, 2, 1, 16), (11, 128, 4, 3, 32), (5, 128, 4, 8, 16),
+    (8, 64, 4, 8, 16), (64, 96, 1, 1, 16), (65, 80, 4, 1, 16), (9, 128, 1, 7, 8)])
 def test_attend_drafted_tokens(dtype, q_len, d, h, group, page):
     """Some new tokens of each sequence, around the sizes at which another way of running them begins;
     unsplit and in splits."""
@@ -515,6 +516,29 @@ def test_attend_keys_shared_out(n_seqs, h, q_len):
         log(f"keys shared out: {n_seqs} sequences, h={h} q={q_len} causal={causal} window={window}")
         out, lse = run_attend(c, 0.25, causal, window, max_kv=max_kv)
         K.check_attention(c, out, lse, K.attention(c, 0.25, causal=causal, window=window), f"window={window}")
+        assert (out[c.n - 1:] == PAD).all() and (lse[c.n - 1:] == PAD).all()
+
+
+@pytest.mark.parametrize("dtype,n_seqs,h,group,d,most", [
+    (BF16, 1, 1, 4, 128, 60), (F16, 3, 2, 3, 64, 130), (BF16, 5, 8, 8, 128, 8), (F16, 20, 2, 2, 80, 100),
+    (BF16, 34, 1, 2, 64, 70), (F16, 70, 2, 1, 128, 140), (BF16, 9, 4, 2, 256, 70), (BF16, 100, 2, 12, 16, 3)])
+def test_chunk_keys_shared_out(monkeypatch, dtype, n_seqs, h, group, d, most):
+    """Chunks of very different lengths against contexts of very different lengths, one or more tiles of rows,
+    most without rows in some cases, whose keys are shared out over workgroups; a workspace of all ones."""
+    monkeypatch.setitem(globals(), "ws", lambda n: torch.full((max(n, 16),), 0xFF, dtype=torch.uint8, device="cuda"))
+    rng = torch.Generator().manual_seed(n_seqs)
+    lens = [(int(torch.randint(0, 1 + (most if s % 3 == 0 else 3), (1,), generator=rng)),
+             int(torch.randint(0, 300, (1,), generator=rng))) for s in range(n_seqs)]
+    lens = [(q, q + kv if s % 7 else kv) for s, (q, kv) in enumerate(lens)]  # (some with fewer keys than rows)
+    lens[n_seqs // 2] = (most, 3000)
+    c = K8.Case8(lens, dtype=dtype, h=h, group=group, d=d, page=16, strange=True, fill=math.nan, tail_rows=1,
+                 seed=n_seqs)
+    for causal, window, max_kv in ((True, 0, None), (True, 1100, None), (False, 0, 9000)):
+        if max_kv:
+            wider_table(c, max_kv)
+        log(f"chunks shared out: {n_seqs} sequences, h={h} group={group} d={d} causal={causal} window={window}")
+        out, lse = run_attend(c, 0.125, causal, window, max_kv=max_kv)
+        K.check_attention(c, out, lse, K.attention(c, 0.125, causal=causal, window=window), f"window={window}")
         assert (out[c.n - 1:] == PAD).all() and (lse[c.n - 1:] == PAD).all()
 
 
