@@ -44,8 +44,9 @@ hipError_t plan8(const Cache8& c, const Batch& b, uint32_t n_q_heads, uint32_t w
   uint64_t keys = b.max_kv;
   if (window && keys > (uint64_t)window + b.max_q) keys = (uint64_t)window + b.max_q;
   const uint64_t tiles = (keys + 31) / 32;
+  // (all sequences' tiles are summed in 32 bits; without the window, as a call with one has no larger workspace)
   if (b.n_seqs && b.n_seqs <= kMaxShared && b.n_seqs < at_once && tiles > 4 &&
-      b.n_seqs * tiles < (1u << 31)) {  // (all sequences' tiles are summed in 32 bits)
+      b.n_seqs * (((uint64_t)b.max_kv + 31) / 32) < (1u << 31)) {
     uint64_t shares = at_once > 2 * (uint64_t)b.n_seqs ? at_once : 2 * (uint64_t)b.n_seqs;
     if (shares > b.n_seqs * tiles) shares = b.n_seqs * tiles;
     if (shares > kMaxSplits) shares = kMaxSplits;
@@ -63,8 +64,8 @@ hipError_t plan8(const Cache8& c, const Batch& b, uint32_t n_q_heads, uint32_t w
 // 1,638 to 8,192 tokens 123 us (94 so), 3 chunks of up to 300 over 2,000 to 20,000 265 (198), 2 of up to 256 over
 // up to 30,000 215 (189); where the lengths are equal, one chunk of 1,024 over 4,096 tokens, 92 (96: each
 // workgroup's look at all lengths).  More rounds of workgroups, where the tiles leave no places: chunks of up to
-// 511 over 9,001 tokens 315 us, 264 with a workgroup a tile.  33 to 64 rows as four columns of k_kv8_decode instead: 124 and 131 us for
-// the first, 140 for 7 sequences over 91,718 tokens that take 92.
+// 511 over 9,001 tokens 315 us, 264 with a workgroup a tile.  33 to 64 rows as four columns of k_kv8_decode
+// instead: 124 and 131 us for the first, 140 for 7 sequences over 91,718 tokens that take 92.
 hipError_t plan_chunk8(const Cache8& c, const Batch& b, uint32_t n_q_heads, uint32_t window, AttendPlan* p,
                        Plan8* plan) {
   DeviceInfo di;
@@ -73,7 +74,8 @@ hipError_t plan_chunk8(const Cache8& c, const Batch& b, uint32_t n_q_heads, uint
   if (e != hipSuccess) return e;
   *plan = Plan8{};
   const uint32_t group = n_q_heads / c.n_heads;
-  const uint64_t items = (uint64_t)b.n_seqs * p->row_tiles, at_once = di.cus * (c.head_dim <= 128 ? 2 : 1) / c.n_heads;
+  const uint64_t items = (uint64_t)b.n_seqs * p->row_tiles;
+  const uint64_t at_once = di.cus * (c.head_dim <= 128 ? 2 : 1) / c.n_heads;
   const uint64_t by_rows = b.n_seqs + (uint64_t)b.n_rows * group / kChunkRows;
   const uint64_t active = items < by_rows ? items : by_rows;  // (more have no rows)
   uint64_t keys = b.max_kv;
@@ -82,7 +84,7 @@ hipError_t plan_chunk8(const Cache8& c, const Batch& b, uint32_t n_q_heads, uint
   p->splits = 1;
   p->blocks = items * c.n_heads;
   if (items && items <= kMaxShared && active < at_once && steps >= 2 * kLeastSteps &&
-      items * steps < (1u << 31)) {  // (all items' steps are summed in 32 bits)
+      items * (((uint64_t)b.max_kv + 63) / 64 + 1) < (1u << 31)) {  // (as above)
     uint64_t shares = active * (steps / kLeastSteps);
     if (shares > at_once) shares = at_once;
     if (shares > kMaxSplits) shares = kMaxSplits;

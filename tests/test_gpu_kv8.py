@@ -542,6 +542,25 @@ def test_chunk_keys_shared_out(monkeypatch, dtype, n_seqs, h, group, d, most):
         assert (out[c.n - 1:] == PAD).all() and (lse[c.n - 1:] == PAD).all()
 
 
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_windows_where_the_longest_context_has_the_largest_length(q_len):
+    """So many sequences of up to 2^30 tokens that their keys are not shared out: no workspace, with a window either."""
+    c = K8.Case8([(q_len, q_len + 40 + 5 * (s % 50)) for s in range(128)], dtype=BF16, h=1, group=1, d=16, page=1024,
+                 block=16, seed=q_len)
+    wide = torch.full((128, (1 << 30) // 1024), -1, dtype=torch.int32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table.cuda()
+    batch = kv.Batch(c.q_start.cuda(), c.kv_len.cuda(), wide, c.max_q, 1 << 30)
+    cache, q = kv8.Cache(*c.pools8()), c.wide_q.cuda()[:, :1]
+    assert kv8.attend_workspace(cache, batch, c.n, 1) == 0
+    for window in (0, 1024, 30):
+        out = torch.full((c.n, 1, c.d), PAD, dtype=BF16, device="cuda")
+        lse = torch.full((c.n, 1), PAD, device="cuda")
+        log(f"largest length q={q_len} window={window}")
+        kv8.attend(cache, batch, q, out, 0.25, lse=lse, window=window)
+        torch.cuda.synchronize()
+        K.check_attention(c, out, lse, K.attention(c, 0.25, window=window), f"window={window}")
+
+
 @pytest.mark.parametrize("q_len", [1, 2, 40])
 def test_attend_many_small_weights(q_len):
     """Thousands of weights far below the largest one: their sum counts, in fp16 too."""
