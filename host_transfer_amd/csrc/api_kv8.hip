@@ -151,7 +151,7 @@ int ibp_kv8_attend(const ibp_kv8_cache* cache, const ibp_kv_batch* batch, uint32
     return set_error(IBP_ERR_SIZE, "%s: out has %u heads, q has %u", name, orow.n_heads, qr.n_heads);
   if (b.n_rows && (orow.p == qr.p || (same_strides(orow, qr) && rows_overlap(orow, qr, b.n_rows, c.head_dim))))
     return set_error(IBP_ERR_SIZE, "%s: out must not overlap q", name);
-  if (!(fabsf(scale) <= 0x1p125f))  // (scores are in the exponent of 2, of fp16 rows of halves: times 2.89)
+  if (!(fabsf(scale) <= 0x1p125f))  // (scores are in the exponent of 2, of keys' halves: times 2.89)
     return set_error(IBP_ERR_SIZE, "%s: scale must be finite, its magnitude at most 2^125", name);
   if (lse && !aligned(lse, 4)) return set_error(IBP_ERR_ALIGN, "%s: misaligned lse", name);
   if ((r = require_device(name))) return r;

@@ -58,28 +58,28 @@ __device__ __forceinline__ uint32_t valid_exponent(uint32_t e) { return min(max(
 // 2^(e - 127), e in [1, 254]
 __device__ __forceinline__ float power_of(uint32_t e) { return __uint_as_float(e << 23); }
 
-// The weights' range over a cache in 8 bits (Base in kv_mfma.h).  In bf16 they are 2^-32 where those of the
-// 16-bit cache are 2^-8: a sum over 2^30 keys of the type's largest values stays below 2^128, and
-// what a weight near the largest makes of a value is no number below fp32's least normal one down to
-// values of 2^-94.
+// The weights' range over a cache in 8 bits (Base in kv_mfma.h).  In bf16 they are 2^-31 where those of the
+// 16-bit cache are 2^-8: a sum over 2^30 keys of the type's largest values (2^24 in k_kv_chunk, where weights may
+// grow to 2^kRoom) stays below 2^128, and what a weight near the largest makes of a value, read as its
+// half, is no number below fp32's least normal one down to values of 2^-94.
 template <typename T>
 struct In8 {};
 template <>
 struct Base<In8<_Float16>> : Base<_Float16> {};
 template <>
 struct Base<In8<__bf16>> {
-  static constexpr float kLift = -32.f, kRoom = -24.f;
+  static constexpr float kLift = -31.f, kRoom = -24.f;
 };
 
-// Codes as 16-bit values, with their block's power of two.  In bf16 as they are; in fp16 half of them, as
-// the largest, 448 * 2^8 of rows that reach 65504, is past that type: scores and outputs are then
-// taken kScale times.
+// Codes as halves of their 16-bit values, with their block's power of two: the largest that rows of a
+// type's numbers are rounded up to, 2^16 and 2^128, are past that type.  Scores and outputs are then taken kScale times.
+// (The conversion takes the power's exponent field alone: 0 is 2^-127.)
 template <typename T>
 struct Read8;
 template <>
 struct Read8<__bf16> {
-  static constexpr float kScale = 1.f;
-  static __device__ __forceinline__ float power(uint32_t e) { return power_of(valid_exponent(e)); }
+  static constexpr float kScale = 2.f;
+  static __device__ __forceinline__ float power(uint32_t e) { return __uint_as_float((valid_exponent(e) - 1) << 23); }
   static __device__ __forceinline__ V8<__bf16> eight(uint32_t a, uint32_t b, float power) {
     typedef __bf16 v2 __attribute__((ext_vector_type(2)));
     const v2 x = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, power, false);

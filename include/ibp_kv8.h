@@ -28,8 +28,8 @@ extern "C" {
  * uint8[n_pages][page_tokens / block_tokens][n_heads], of k and of v.
  *   block_tokens  divides page_tokens: tokens b * block_tokens and on of a page share exponent b.
  *   head_dim      a multiple of 16 in [16, IBP_KV_MAX_HEAD_DIM].
- *   Exponents are in [1, 254] (0 is read as 1, 255 as 254).  With rows of IBP_KV_F16 a value past
- *   that type's range is read as up to twice its largest number, and as an infinity beyond.
+ *   Exponents are in [1, 254] (0 is read as 1, 255 as 254).  A value past the range of the rows' type is
+ *   read as up to twice the type's largest number, and as an infinity beyond.
  * No two rows may overlap (IBP_ERR_SIZE). */
 typedef struct {
     void *k, *v;
@@ -71,9 +71,10 @@ int ibp_kv8_append(const ibp_kv8_cache *cache, const ibp_kv_batch *batch, uint32
 /*
  * ibp_kv8_attend -- ibp_kv_attend over a cache in 8 bits: the same rows, masks, outputs, log of the
  * sums and refusals (but scale at most 2^125), with K and V the values that the codes and exponents
- * stand for.  They are exact in the rows' type, but in IBP_KV_F16 below 2^-20, where they are
- * rounded to multiples of 2^-23, and in IBP_KV_BF16 values of V below 2^-94 and of K below 2^-126,
- * which may be taken as zero.
+ * stand for.  They are exact in the rows' type and somewhat past its range (above), but in IBP_KV_F16 below
+ * 2^-20, where they are rounded to multiples of 2^-23, and in IBP_KV_BF16 values of V below 2^-94 and of K
+ * below 2^-125, which may be taken as zero.  An output is the type's largest number at most, where its row sees
+ * no value that is read as an infinity or NaN.
  *   workspace   ibp_kv8_attend_workspace() bytes, 16 B aligned (NULL if 0).
  */
 int ibp_kv8_attend(const ibp_kv8_cache *cache, const ibp_kv_batch *batch, uint32_t dtype,

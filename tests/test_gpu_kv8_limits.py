@@ -1,0 +1,82 @@
+"""The 8-bit paged K/V cache on the GPU at the ends of what its header allows: values next to the rows'
+type's range."""
+import math
+
+import pytest
+import torch
+
+from host_transfer_amd import kv8
+from tests import kv8_case as K8
+from tests import kv_case as K
+from tests.test_gpu_kv8 import gpu_batch, log, run_attend
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+MOST = torch.finfo(BF16).max
+
+
+@pytest.mark.parametrize("q_len,h,n", [(1, 1, 300), (2, 4, 300), (1, 4, 3000), (40, 2, 300), (40, 2, 3000)])
+def test_bf16_values_next_to_the_range(q_len, h, n):
+    """Appended bf16 values past 1.9375 * 2^127 are next to the code of 2^128, which is no bf16 number: they are
+    read as what they stand for, and their mean is the type's largest number at most."""
+    c = K8.Case8([(q_len, n), (q_len, 77)], dtype=BF16, d=64, h=h, group=2, page=16)
+    c.ke[:] = 100  # scores near zero: equal weights
+    rows = torch.full((c.n, 2 * h, 64), MOST, dtype=BF16)
+    rows[:, :, 1::4] = -MOST
+    rows[:, :, 2] = 1.0
+    pools = c.pools8()
+    cache, batch = kv8.Cache(*pools), gpu_batch(c)
+    gpu = rows.cuda()
+    kv8.append(cache, batch, gpu[:, :h], gpu[:, h:])
+    c.v8, c.ve = pools[1].view(torch.uint8).cpu().view(K8.E4M3), pools[3].cpu()
+    c.renew()
+    new = c.v[int(c.table[0, (n - 1) // 16]), (n - 1) % 16]
+    assert (new[:, 0] == 2.0 ** 128).all() and (new[:, 1] == -2.0 ** 128).all()
+    assert torch.equal(c.v8.float()[int(c.table[0, (n - 1) // 16]), (n - 1) % 16, :, 0], torch.full((h,), 256.0))
+    for code, e in ((None, 0), (0x78, 247), (0x7E, 247), (0xFE, 247), (0x77, 247), (0x7F, 247)):
+        if code is not None:
+            c.v8.view(torch.uint8)[:], c.ve[:] = code, e
+            c.renew()
+        log(f"bf16 ends q={q_len} h={h} n={n} code={code}")
+        ref = list(K.attention(c, 0.01))
+        ref[0] = ref[0].clamp(-MOST, MOST)
+        K.check_attention(c, *run_attend(c, 0.01), ref, f"code={code}")
+
+
+@pytest.mark.parametrize("q_len,h,n", [(1, 1, 300), (2, 4, 300), (1, 4, 3000), (40, 2, 300), (40, 2, 3000)])
+def test_bf16_values_past_the_range(q_len, h, n):
+    """Values from twice the type's largest number on: infinities of the rows that see them."""
+    c = K8.Case8([(q_len, n), (q_len, 77)], dtype=BF16, d=64, h=h, group=2, page=16, block=1)
+    for s, j, code, e in ((0, 5, 0x78, 248), (0, n - 2, 0x7E, 254), (1, 3, 0xFE, 255), (1, 9, 0xF0, 248)):
+        at = int(c.table[s, j // 16]), j % 16
+        c.v8.view(torch.uint8)[at] = 0
+        c.v8.view(torch.uint8)[at][:, (7 * j) % 64] = code
+        c.ve[at] = e
+    c.renew()
+    c.v[c.v.abs() > 1.99 * 2.0 ** 128] *= math.inf  # 0xF0 with 248 is -2^128, read as it is
+    for window in (0, 60):
+        log(f"bf16 past the range q={q_len} h={h} n={n} window={window}")
+        K.check_attention(c, *run_attend(c, 0.1, window=window), K.attention(c, 0.1, window=window), f"window={window}")
+
+
+@pytest.mark.parametrize("q_len,h,n", [(1, 1, 300), (2, 4, 300), (40, 2, 300)])
+@pytest.mark.parametrize("e,code,q", [(247, 0x78, 2.0 ** -124), (247, 0x7E, 2.0 ** -124), (246, 0x7E, 2.0 ** -124),
+                                      (1, 0x7E, 2.0 ** 120), (1, 0x40, 2.0 ** 126), (2, 0x7E, 2.0 ** 119),
+                                      (3, 0x7E, 2.0 ** 118)])
+def test_bf16_keys_at_the_ends(q_len, h, n, e, code, q):
+    """Keys next to the upper end of bf16 and of the least exponents, where small and large queries meet them."""
+    c = K8.Case8([(q_len, n), (q_len, 77)], dtype=BF16, d=64, h=h, group=2, page=16, block=1)
+    c.q[:] = 0
+    c.q[..., 0], c.q[..., 1] = q, 1.0
+    c.k8.view(torch.uint8)[:], c.ke[:] = 0, 127
+    for s, j in ((0, 5), (0, 70), (0, 200), (1, 2), (1, 30)):
+        at = int(c.table[s, j // 16]), j % 16
+        c.k8.view(torch.uint8)[at][:, 0] = code + (0x80 if j == 70 else 0)
+        c.ke[at] = e
+    c.k8.view(torch.uint8)[int(c.table[0, 1]), 0][:, 1] = 0x48  # 4, of a block of exponent 127
+    c.renew()
+    scale = 0.25 * 64 / abs(float(c.k[int(c.table[0, 0]), 5, 0, 0]) * q)  # scores of 16, -16, 16
+    log(f"bf16 keys at the ends q={q_len} h={h} e={e} code={code}")
+    K.check_attention(c, *run_attend(c, scale), K.attention(c, scale), f"e={e}")
+
