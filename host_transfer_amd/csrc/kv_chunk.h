@@ -81,6 +81,8 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // products.  No faster: conversions between the values' products (1,312 where this then took 1,304), lanes in an
 // order that meets no bank twice (1 % slower by its selections), codes in registers without a stage (395 us of
 // ragged chunks: they do not fit beside the products').
+// Registers are just enough (253 and 255 of 256 at DP 128): a reload inside the loop waits for the
+// rows on their way too (ragged chunks of heads of 112 286 us with eight in two steps, fp16, 275 without).
 template <typename T, int DP, bool kExact, typename C>  // kExact: head_dim == DP == the LDS row
 __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     C cache, Batch b, Rows q, Rows out, float scale, uint32_t window, bool causal,
@@ -200,9 +202,9 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   const uint32_t wm0 = min(m0 + wave * 32, m1 - 1), wm1 = min(m0 + wave * 32 + 32, m1) - 1;
   const int32_t full_lo = lo_of(pos_of(active ? wm1 : wm0)), full_hi = hi_of(pos_of(wm0));
   const bool have = m0 + wave * 32 + col < m1;
-  const uint32_t m = have ? m0 + wave * 32 + col : m1 - 1;
+  uint32_t m = have ? m0 + wave * 32 + col : m1 - 1;
   const int32_t pos = pos_of(m), lo = lo_of(pos), hi = hi_of(pos);
-  const uint32_t row = (uint32_t)sq.row0 + m / group, head = kh * group + m % group;
+  uint32_t row = (uint32_t)sq.row0 + m / group, head = kh * group + m % group;
 
   const int32_t from = blk_lo / kKeys * kKeys;
   const int32_t tiles = max(blk_hi - from + kKeys - 1, 0) / kKeys;
@@ -270,20 +272,21 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     const int32_t j = t0 + (int32_t)lane;
     return t0 < end && j >= blk_lo && j < blk_hi ? table[cache.page.div((uint32_t)j)] : -1;
   };
-  // where key t0 + lane lies (elements), and which of the 64 are there
+  // where key t0 + lane lies (elements; a cache in 8 bits: ~0 where it does not, which takes fewer registers
+  // than masks of the loads' rows), and which of the 64 are there
   auto locate = [&](int32_t t0, int32_t id, uint64_t& at) -> uint64_t {
     const uint32_t j = (uint32_t)(t0 + (int32_t)lane);
     const bool see = id >= 0 && (uint32_t)id < cache.n_pages;
     at = see ? (uint64_t)(uint32_t)id * cache.page_stride +
                    (uint64_t)(j - cache.page.div(j) * cache.page.d) * cache.token_stride
-             : 0;
+             : kEight ? ~0ull : 0;
     return __ballot(see);
   };
   // exponents of key t0 + lane's block (0, any, where it is not there)
-  auto exponents = [&](int32_t t0, int32_t id, uint64_t seen, uint32_t& ke, uint32_t& ve) {
+  auto exponents = [&](int32_t t0, int32_t id, uint32_t& ke, uint32_t& ve) {
     ke = ve = 0;
     if constexpr (kEight) {
-      if ((seen >> lane) & 1u) {
+      if ((uint32_t)id < cache.n_pages) {
         const uint32_t j = (uint32_t)(t0 + (int32_t)lane), in = j - cache.page.div(j) * cache.page.d;
         const uint64_t at = ((uint64_t)(uint32_t)id * cache.page_blocks + cache.block.div(in)) * cache.n_heads + kh;
         ke = cache.k_exp[at];
@@ -309,7 +312,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
         const uint32_t r = first + i * RPR8;
         const uint64_t a = ((uint64_t)(uint32_t)__shfl((int)(uint32_t)(at >> 32), (int)r) << 32) |
                            (uint32_t)__shfl((int)(uint32_t)at, (int)r);
-        const void* p = (seen >> r) & 1u ? (const void*)(base + a + c) : (const void*)zeros;
+        const void* p = a != ~0ull ? (const void*)(base + a + c) : (const void*)zeros;
         if (kExact || c < hd) load_lds(p, stage + i * (kThreads * 16));
       }
     }
@@ -477,8 +480,8 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     const int32_t id0 = lookup(begin), id1 = lookup(begin + kKeys);
     seen0 = locate(begin, id0, at0);
     seen1 = locate(begin + kKeys, id1, at1);
-    exponents(begin, id0, seen0, ke0, ve0);
-    exponents(begin + kKeys, id1, seen1, ke1, ve1);
+    exponents(begin, id0, ke0, ve0);
+    exponents(begin + kKeys, id1, ke1, ve1);
     if (!kEight && tid == 0) s_odd = s_bad = 0;
     lds_barrier();
     if (begin < end) {
@@ -518,7 +521,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   // in the step before or ahead of the loop) and of s_v[buf ^ 1] (the values of t0 - 64).
   auto step = [&](int32_t t0, uint32_t buf, f32x16 (&cur)[2], f32x16 (&nxt)[2]) {
     seen2 = locate(t0 + 2 * kKeys, id2, at2);
-    exponents(t0 + 2 * kKeys, id2, seen2, ke2, ve2);
+    exponents(t0 + 2 * kKeys, id2, ke2, ve2);
     if (t0 + kKeys < end) bring(vbase, at1, seen1, lds_v + (buf ^ 1) * TILE * 2, false);
     if (t0 + 2 * kKeys < end) bring(kbase, at2, seen2, lds_k + buf * TILE * 2, true);
     id2 = lookup(t0 + 3 * kKeys);
@@ -623,7 +626,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       wait_loads();
       if constexpr (kEight) {
         uint32_t ke, ve;
-        exponents(t0, id, seen, ke, ve);
+        exponents(t0, id, ke, ve);
         unpack(s_v[0], ve, false);
       }
       lds_barrier();
@@ -657,7 +660,15 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
     }
   }
 
-  if (!have) return;
+  if constexpr (kEight) {  // found again, so that no registers hold them through the loop
+    uint32_t t = threadIdx.x;
+    asm("" : "+v"(t));
+    m = m0 + t / kWave * 32 + t % 32;
+    row = (uint32_t)sq.row0 + m / group;
+    head = kh * group + m % group;
+    if (m >= m1) return;
+  }
+  if (!kEight && !have) return;
   if (kEight && Read8<T>::kScale != 1.f)
 #pragma unroll
     for (int t = 0; t < DT; ++t)
