@@ -60,16 +60,23 @@ __device__ __forceinline__ float power_of(uint32_t e) { return __uint_as_float(e
 
 // The weights' range over a cache in 8 bits (Base in kv_mfma.h).  In bf16 they are 2^-31 where those of the
 // 16-bit cache are 2^-8: a sum over 2^30 keys of the type's largest values (2^24 in k_kv_chunk, where weights may
-// grow to 2^kRoom) stays below 2^128, and what a weight near the largest makes of a value, read as its
-// half, is no number below fp32's least normal one down to values of 2^-94.
+// grow by 2^kRoom) stays below 2^128, and what a weight near the largest makes of a value, read as its
+// half, is no number below fp32's least normal one down to values of 2^-94.  They are so for scores of any
+// size, as weights of 1 would let two of the largest values pass 2^128: the 31 are no part of the base, which is the
+// largest score (to the last place of base + 31, so that this sum is exact).  With bases up to 2^20 a weight
+// is 2^(score - (base + 31)), beyond 2^((score - base) - 31).
 template <typename T>
 struct In8 {};
 template <>
 struct Base<In8<_Float16>> : Base<_Float16> {};
 template <>
 struct Base<In8<__bf16>> {
-  static constexpr float kLift = -31.f, kRoom = -24.f;
+  static constexpr float kLift = 0.f, kRoom = 7.f, kBeside = 31.f;
 };
+template <>
+__device__ __forceinline__ float next_base<In8<__bf16>>(float base, float most) {
+  return fmaxf(base, (most + Base<In8<__bf16>>::kBeside) - Base<In8<__bf16>>::kBeside);
+}
 
 // Codes as halves of their 16-bit values, with their block's power of two: the largest that rows of a
 // type's numbers are rounded up to, 2^16 and 2^128, are past that type.  Scores and outputs are then taken kScale times.

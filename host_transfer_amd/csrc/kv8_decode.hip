@@ -290,7 +290,16 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
           for (int r = 0; r < 4; ++r) o[n][t][r] *= keep;
         top[n] = next;
       }
-      const float base = top[n] == -INFINITY ? 0.f : top[n];
+      float base = top[n] == -INFINITY ? 0.f : top[n];
+      if (Base<In8<T>>::kBeside != 0.f) {
+#pragma clang fp contract(off)
+        if (__any(fabsf(base) >= 0x1p20f)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] -= base;
+          base = 0.f;
+        }
+        base += Base<In8<T>>::kBeside;
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
 // (the product rounded as the base was: the largest of huge scores, too, is the base itself)
@@ -425,7 +434,7 @@ __global__ __launch_bounds__(256, decode8_groups(DP, NC)) void k_kv8_decode(
     }
     if (first_c == 0) {
       if (!whole) plan.ms[slot] = make_float2(mm, zz);
-      else if (lse) lse[unit] = zz == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(zz)) * kLn2;
+      else if (lse) lse[unit] = zz == 0.f ? -INFINITY : (log_of_base<In8<T>>(mm) + __builtin_amdgcn_logf(zz)) * kLn2;
     }
   }
 }
@@ -470,7 +479,8 @@ __device__ __forceinline__ void finish(const Rows& out, uint32_t row, uint32_t h
     *(t4*)((T*)out.p + row * out.token_stride + (uint64_t)head * out.head_stride + c) = v;
   }
   if (lse && c == 0)
-    lse[(uint64_t)row * out.n_heads + head] = z == 0.f ? -INFINITY : (mm + __builtin_amdgcn_logf(z)) * kLn2;
+    lse[(uint64_t)row * out.n_heads + head] =
+        z == 0.f ? -INFINITY : (log_of_base<In8<T>>(mm) + __builtin_amdgcn_logf(z)) * kLn2;
 }
 
 // The splits of rows together: a wave to one row of an item and key head, 64 splits' factors in its lanes, then

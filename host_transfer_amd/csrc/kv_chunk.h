@@ -97,6 +97,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   constexpr int TILE = kKeys * DL;
   constexpr bool kEight = __is_same(C, Shared8);
   typedef std::conditional_t<kEight, In8<T>, T> W;  // what the weights' range goes by
+  constexpr float kBeside = Base<W>::kBeside;
   constexpr int CH8 = DL / 16, ST8 = kKeys * CH8 / kThreads;  // the same of codes: 16 to a piece
   constexpr int RPL8 = kWave / CH8, RPR8 = kThreads / CH8;
   __shared__ __align__(1024) uint16_t s_k[2][TILE];
@@ -460,15 +461,29 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       top = next;
     }
     mul = sc2;
-    off = top == -INFINITY ? 0.f : -top;
-    if (__any(fabsf(off) >= 0x1p20f)) {
+    if constexpr (kBeside == 0.f) {
+      off = top == -INFINITY ? 0.f : -top;
+      if (__any(fabsf(off) >= 0x1p20f)) {
 #pragma clang fp contract(off)
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) sc[a][r] = sc[a][r] * sc2 + off;
-      mul = 1.f;
-      off = 0.f;
+          for (int r = 0; r < 16; ++r) sc[a][r] = sc[a][r] * sc2 + off;
+        mul = 1.f;
+        off = 0.f;
+      }
+    } else {
+      off = top == -INFINITY ? -kBeside : -kBeside - top;
+      if (__any(fabsf(top) >= 0x1p20f && top != -INFINITY)) {
+#pragma clang fp contract(off)
+        const float ref = top == -INFINITY ? 0.f : -top;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sc[a][r] = sc[a][r] * sc2 + ref;
+        mul = 1.f;
+        off = -kBeside;
+      }
     }
   };
 
@@ -713,7 +728,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
       for (int e = 0; e < 4; ++e) v[e] = mean<T>(o[t][4 * r + e], inv);
       if (c < hd) *(t4*)(op + c) = v;
     }
-  if (lse && half == 0) lse[unit] = z == 0.f ? -INFINITY : (top + __builtin_amdgcn_logf(z)) * kLn2;
+  if (lse && half == 0) lse[unit] = z == 0.f ? -INFINITY : (log_of_base<W>(top) + __builtin_amdgcn_logf(z)) * kLn2;
 }
 
 }  // namespace

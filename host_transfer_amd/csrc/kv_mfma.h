@@ -107,20 +107,26 @@ __device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp
 // 2^-26 of the largest one still has all of it, and what is lost of n smaller ones is below n * 2^-37
 // of the largest (with weights up to 1 it was n * 2^-25: 30,000 weights of 2^-25, 7.5e-4 of
 // the sum together, came out 2 % short).  Scores past 2^20 are the base themselves: their
-// distance to another base would be rounded by more than the room can bear.
+// distance to another base would be rounded by more than the room can bear.  kBeside: what a weight,
+// 2^(score - base - kBeside), has taken off beside its base (kv8.h).
 template <typename T>
 struct Base;
 template <>
 struct Base<_Float16> {
-  static constexpr float kLift = 12.f, kRoom = 15.f;
+  static constexpr float kLift = 12.f, kRoom = 15.f, kBeside = 0.f;
 };
 template <>
 struct Base<__bf16> {
-  static constexpr float kLift = -8.f, kRoom = 0.f;
+  static constexpr float kLift = -8.f, kRoom = 0.f, kBeside = 0.f;
 };
 template <typename T>
 __device__ __forceinline__ float next_base(float base, float most) {
   return fmaxf(base, fabsf(most) < 0x1p20f ? most - Base<T>::kLift : most);
+}
+// The score whose weight is 1.
+template <typename T>
+__device__ __forceinline__ float log_of_base(float base) {
+  return Base<T>::kBeside == 0.f ? base : base + Base<T>::kBeside;
 }
 
 // 16 B from global memory through a global-address-space pointer.

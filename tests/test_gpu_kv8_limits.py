@@ -1,5 +1,5 @@
 """The 8-bit paged K/V cache on the GPU at the ends of what its header allows: values next to the rows'
-type's range."""
+type's range, scores of any size."""
 import math
 
 import pytest
@@ -80,3 +80,56 @@ def test_bf16_keys_at_the_ends(q_len, h, n, e, code, q):
     log(f"bf16 keys at the ends q={q_len} h={h} e={e} code={code}")
     K.check_attention(c, *run_attend(c, scale), K.attention(c, scale), f"e={e}")
 
+
+H = 2.0 ** 24  # scores (in the exponent of 2) are whole numbers from here on
+
+
+@pytest.mark.parametrize("q_len,h,n", [(1, 1, 300), (2, 4, 300), (1, 4, 3000), (1, 1, 9000), (3, 8, 9000), (40, 2, 300),
+                                       (40, 2, 3000), (40, 1, 20000)])
+@pytest.mark.parametrize("high", [1.0, 2.0 ** 17, 2.0 ** 20 - 31, 2.0 ** 20, 2.0 ** 22, H - 40, H - 31, H - 16, H - 1, H, H + 1,
+                                  H + 40, 2.0 ** 30, 2.0 ** 60])
+def test_large_values_under_equal_scores(q_len, h, n, high):
+    """Keys that share the largest score, of any size, with values near the type's largest: a mean, wherever the scores
+    lie; other keys' scores are far below, in front of and behind them.
+
+    A row's output is the mean of the values whose score is its largest (the others' weights are 0). Weights of
+    equal scores are equal; each is rounded to bf16 for the product and not in their sum (u), the sums carry
+    (n + 8) U32, the output is rounded once (u); the tolerance is twice their sum, as second-order terms are no
+    more than that.  lse: the score carries the rounding of scale * log2(e) (2 U32), of the product, of the base, of ln 2
+    and of two products with it: 8 U32 of its magnitude, and the sum's (n + 8) U32."""
+    c = K8.Case8([(q_len, n), (q_len, 130)], dtype=BF16, d=16, h=h, group=2, page=16)
+    scale = high / math.log2(math.e)
+    c.q[:] = 0
+    c.q[..., 0] = 1.0
+    g = torch.Generator().manual_seed(n)
+    # levels of the keys' scores, -scale, 0 or scale: eight by eight at random; -scale but for eight of 0
+    levels = [torch.randint(-1, 2, (n // 8 + 1,), generator=g).repeat_interleave(8)[:n], torch.full((130,), -1)]
+    levels[1][40:48] = 0
+    if high < 100:
+        levels = [torch.ones_like(x) for x in levels]
+    k8 = c.k8.view(torch.uint8).view(-1, h, 16)
+    k8[:] = 0
+    for s, level in enumerate(levels):
+        j = torch.arange(len(level))
+        k8[c.table[s].long()[j // 16] * 16 + j % 16, :, 0] = torch.tensor([0xB8, 0, 0x38], dtype=torch.uint8)[level + 1][:, None]
+    c.ke[:] = 127
+    c.v8.view(torch.uint8)[:] = torch.where(torch.rand(c.v8.shape, generator=g) < 0.9, 0x7E, 0x70).to(torch.uint8)
+    c.ve[:] = 246
+    c.renew()
+    u, U = torch.finfo(BF16).eps / 2, K.U32
+    for window in (0, 33):
+        log(f"equal scores q={q_len} h={h} n={n} high={high} window={window}")
+        out, lse = run_attend(c, scale, window=window)
+        out, lse = out.cpu().double(), lse.cpu().double()
+        for r, s, pos in c.rows():
+            lv = levels[s]
+            lo = max(pos - window + 1, 0) if window else 0
+            top = lv[lo:pos + 1].max()
+            j = lo + (lv[lo:pos + 1] == top).nonzero().flatten()
+            ids = c.table[s].long()[j // 16]
+            want = c.v[ids, j % 16].mean(0)  # (h, d)
+            want = want.repeat_interleave(2, 0)
+            tol = 2 * (2 * u + (n + 8) * U)
+            assert ((out[r] - want).abs() <= tol * want).all(), (r, window, float((out[r] / want - 1).abs().max()))
+            want_lse = scale * float(top) + math.log(len(j))
+            assert ((lse[r] - want_lse).abs() <= 8 * U * abs(scale * float(top)) + (n + 8) * U + 8 * U * abs(want_lse)).all()
