@@ -6,16 +6,6 @@ namespace kv {
 
 namespace {
 
-// What the plan over a cache in 16 bits (kv_attend.hip) asks of one.
-Cache geometry(const Cache8& c) {
-  Cache g = {};
-  g.n_pages = c.n_pages;
-  g.n_heads = c.n_heads;
-  g.head_dim = c.head_dim;
-  g.page = c.page;
-  return g;
-}
-
 bool few_rows(const Cache8& c, const Batch& b, uint32_t n_q_heads) {
   return (uint64_t)b.max_q * (n_q_heads / c.n_heads) <= 32;
 }
@@ -58,9 +48,9 @@ hipError_t plan8(const Cache8& c, const Batch& b, uint32_t n_q_heads, uint32_t w
   return (uint64_t)p->places * (c.n_heads / p->head_group) > 0xFFFFFFull ? hipErrorInvalidConfiguration : hipSuccess;
 }
 
-// Many rows, as over a cache in 16 bits but for the splits: where the row tiles leave places among the workgroups
-// that the GPU runs at a time, the keys of all tiles are shared out over these by their lengths, which differ
-// between sequences.  Equal numbers of splits for all tiles took: 24 sequences of 5 to 9 rows for 8 heads each over
+// Many rows, as over a cache in 16 bits (kv_attend.hip) but for the splits: where the row tiles leave places among
+// the workgroups that the GPU runs at a time, the keys of all tiles are shared out over these by their lengths,
+// which differ between sequences.  Equal numbers of splits for all tiles took: 24 sequences of 5 to 9 rows for 8 heads each over
 // 1,638 to 8,192 tokens 123 us (94 so), 3 chunks of up to 300 over 2,000 to 20,000 265 (198), 2 of up to 256 over
 // up to 30,000 215 (189); where the lengths are equal, one chunk of 1,024 over 4,096 tokens, 92 (96: each
 // workgroup's look at all lengths).  More rounds of workgroups, where the tiles leave no places: chunks of up to
@@ -70,10 +60,12 @@ hipError_t plan_chunk8(const Cache8& c, const Batch& b, uint32_t n_q_heads, uint
                        Plan8* plan) {
   DeviceInfo di;
   hipError_t e = device_info(&di);
-  if (e == hipSuccess) e = make_plan(geometry(c), b, n_q_heads, 0, window, p);
   if (e != hipSuccess) return e;
   *plan = Plan8{};
+  *p = AttendPlan{};
   const uint32_t group = n_q_heads / c.n_heads;
+  p->row_tiles = (uint32_t)(((uint64_t)b.max_q * group + kChunkRows - 1) / kChunkRows);
+  p->by_length = longest_first(b);
   const uint64_t items = (uint64_t)b.n_seqs * p->row_tiles;
   const uint64_t at_once = di.cus * (c.head_dim <= 128 ? 2 : 1) / c.n_heads;
   const uint64_t by_rows = b.n_seqs + (uint64_t)b.n_rows * group / kChunkRows;
@@ -81,7 +73,6 @@ hipError_t plan_chunk8(const Cache8& c, const Batch& b, uint32_t n_q_heads, uint
   uint64_t keys = b.max_kv;
   if (window && keys > (uint64_t)window + b.max_q) keys = (uint64_t)window + b.max_q;
   const uint64_t steps = (keys + 63) / 64 + 1;
-  p->splits = 1;
   p->blocks = items * c.n_heads;
   if (items && items <= kMaxShared && active < at_once && steps >= 2 * kLeastSteps &&
       items * (((uint64_t)b.max_kv + 63) / 64 + 1) < (1u << 31)) {  // (as above)

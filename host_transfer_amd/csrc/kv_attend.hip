@@ -5,6 +5,8 @@
 namespace ibp {
 namespace kv {
 
+namespace {
+
 // How a call is run.
 //   few    Up to 16 rows share a sequence's keys (one new token, or a few, with its group of
 //          heads), or each row has its own list of pages.
@@ -43,8 +45,7 @@ hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_
   if (splits > kMaxSplits) splits = kMaxSplits;
   p->splits = splits < 1 ? 1 : (uint32_t)splits;
   p->blocks = base * p->splits;
-  p->by_length = !p->few && b.n_seqs > 1 && b.n_seqs <= (uint32_t)kWave &&
-                 (uint64_t)b.max_q * 2 <= b.max_kv;
+  p->by_length = !p->few && longest_first(b);
   // a launch's threads are counted in 32 bits: 256 a workgroup, up to 1024 a row where many
   // splits are joined
   const uint64_t units = (uint64_t)b.n_rows * n_q_heads;
@@ -57,6 +58,8 @@ uint64_t partial_bytes(const Cache& c, const Batch& b, uint32_t n_q_heads, const
   if (p.splits == 1) return 0;
   return (uint64_t)b.n_rows * n_q_heads * p.splits * (c.head_dim + 2) * 4;
 }
+
+}  // namespace
 
 hipError_t attend_workspace(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
                             uint64_t* bytes) {

@@ -230,10 +230,10 @@ struct AttendPlan {
   uint64_t blocks;
 };
 
-// kv_attend.hip
-hipError_t make_plan(const Cache& c, const Batch& b, uint32_t n_q_heads, uint32_t n_select,
-                     uint32_t window, AttendPlan* p);
-uint64_t partial_bytes(const Cache& c, const Batch& b, uint32_t n_q_heads, const AttendPlan& p);
+// Whether k_kv_chunk takes the longest sequences' tiles first (why: kv_attend.hip).
+inline bool longest_first(const Batch& b) {
+  return b.n_seqs > 1 && b.n_seqs <= 64 && (uint64_t)b.max_q * 2 <= b.max_kv;
+}
 
 hipError_t launch_decode(const AttendPlan& p, const Cache& c, uint32_t dtype, const Batch& b,
                          const Rows& q, const Rows& out, const int32_t* sel, uint32_t n_select,

@@ -1,5 +1,5 @@
 """The 8-bit paged K/V cache on the GPU at the ends of what its header allows: values next to the rows'
-type's range, scores of any size."""
+type's range, scores of any size, batches with far more rows than tokens."""
 import math
 
 import pytest
@@ -8,7 +8,7 @@ import torch
 from host_transfer_amd import kv8
 from tests import kv8_case as K8
 from tests import kv_case as K
-from tests.test_gpu_kv8 import gpu_batch, log, run_attend
+from tests.test_gpu_kv8 import PAD, gpu_batch, log, run_attend, wider_table, ws
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +133,18 @@ def test_large_values_under_equal_scores(q_len, h, n, high):
             assert ((out[r] - want).abs() <= tol * want).all(), (r, window, float((out[r] / want - 1).abs().max()))
             want_lse = scale * float(top) + math.log(len(j))
             assert ((lse[r] - want_lse).abs() <= 8 * U * abs(scale * float(top)) + (n + 8) * U + 8 * U * abs(want_lse)).all()
+
+
+def test_few_new_tokens_in_a_batch_of_many_rows():
+    """A chunk in a batch whose rows are mostly of no sequence (a buffer of the largest step's size)."""
+    c = K8.Case8([(2, 2000)], dtype=BF16, d=16, h=1, group=32, page=16, tail_rows=139_998)
+    wider_table(c, 40_000)
+    log("few new tokens in a batch of many rows")
+    cache, batch = kv8.Cache(*c.pools8()), gpu_batch(c, max_kv=40_000)
+    q = c.wide_q.cuda()[:, :32]
+    out = torch.full((c.n, 32, 16), PAD, dtype=BF16, device="cuda")
+    lse = torch.full((c.n, 32), PAD, device="cuda")
+    kv8.attend(cache, batch, q, out, 0.25, lse=lse, workspace=ws(kv8.attend_workspace(cache, batch, c.n, 32)))
+    torch.cuda.synchronize()
+    K.check_attention(c, out, lse, K.attention(c, 0.25))
+    assert (out[2:] == PAD).all() and (lse[2:] == PAD).all()
