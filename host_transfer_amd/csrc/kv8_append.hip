@@ -138,7 +138,7 @@ __global__ __launch_bounds__(256, 4) void k_kv8_append(Cache8 cache, Batch b, Ro
   typedef V8<T> v8;
   const uint32_t lane = threadIdx.x % kWave, c = lane % L, sub = lane / L;
   const Pieces p = pieces_of(t, c);
-  uint64_t u = (uint64_t)blockIdx.x * kWaves + uniform(threadIdx.x / kWave);
+  uint64_t u = ((uint64_t)blockIdx.y * gridDim.x + blockIdx.x) * kWaves + uniform(threadIdx.x / kWave);
   if (u < kv_units) {
     const uint32_t side = kHeads ? (cache.n_heads + HW - 1) / HW : cache.n_heads;  // units of K, of V
     const uint32_t hh = (uint32_t)(u % (2 * side));
@@ -336,10 +336,13 @@ hipError_t run_append8(const Cache8& c, const Batch& b, const Rows& k, const Row
   if (parts == 0) parts = 1;
   const uint64_t units = kv_units + (q.n_heads ? (uint64_t)b.n_rows * parts : 0);
   const uint64_t blocks = (units + kWaves - 1) / kWaves;
-  if (blocks > 0xFFFFFFull) return hipErrorInvalidConfiguration;
+  // (one dimension's threads are counted in 32 bits; waves past the last unit find no row)
+  const uint64_t layers = (blocks + 0xFFFFFEull) / 0xFFFFFFull;
+  if (layers > 65535) return hipErrorInvalidConfiguration;
+  const dim3 grid((uint32_t)((blocks + layers - 1) / layers), (uint32_t)layers);
   auto launch = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks), dim3(256), 0, s, c, b, k, v, q, q_out, t, (const T*)q_norm,
-                       (const T*)k_norm, seq_blocks, kv_units, parts);
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, c, b, k, v, q, q_out, t, (const T*)q_norm, (const T*)k_norm,
+                       seq_blocks, kv_units, parts);
     return hipGetLastError();
   };
   return by_heads ? launch(k_kv8_append<T, L, true>) : launch(k_kv8_append<T, L, false>);

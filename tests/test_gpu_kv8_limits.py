@@ -1,11 +1,12 @@
 """The 8-bit paged K/V cache on the GPU at the ends of what its header allows: values next to the rows'
-type's range, scores of any size, batches with far more rows than tokens."""
+type's range, scores of any size, batches with far more rows than tokens, more workgroups than one dimension
+of a launch takes."""
 import math
 
 import pytest
 import torch
 
-from host_transfer_amd import kv8
+from host_transfer_amd import kv, kv8
 from tests import kv8_case as K8
 from tests import kv_case as K
 from tests.test_gpu_kv8 import PAD, gpu_batch, log, run_attend, wider_table, ws
@@ -148,3 +149,25 @@ def test_few_new_tokens_in_a_batch_of_many_rows():
     torch.cuda.synchronize()
     K.check_attention(c, out, lse, K.attention(c, 0.25))
     assert (out[2:] == PAD).all() and (lse[2:] == PAD).all()
+
+
+def test_append_more_blocks_than_a_launch_dimension():
+    """2^26 (block, K or V, head)s: a wave each, four to a workgroup, so more workgroups than 2^24 - 1."""
+    n, h, d, page = 1 << 19, 64, 16, 64
+    n_pages = n // page
+    k8, v8 = (torch.full((n_pages, page, h, d), 0x55, dtype=torch.uint8, device="cuda") for _ in "kv")
+    ke, ve = (torch.zeros((n_pages, page, h), dtype=torch.uint8, device="cuda") for _ in "kv")
+    table = torch.randperm(n_pages, generator=torch.Generator().manual_seed(1)).int().cuda()[None]
+    batch = kv.Batch(torch.tensor([0, n], dtype=torch.int32, device="cuda"),
+                     torch.tensor([n], dtype=torch.int32, device="cuda"), table, n, n)
+    # one row for all tokens
+    one = torch.randn((1, 2 * h, d), generator=torch.Generator().manual_seed(2)).to(BF16).cuda()
+    rows = one.expand(n, 2 * h, d)
+    log("append of 2^26 blocks")
+    kv8.append(kv8.Cache(k8.view(K8.E4M3), v8.view(K8.E4M3), ke, ve), batch, rows[:, :h], rows[:, h:])
+    torch.cuda.synchronize()
+    for codes, exps, x in ((k8, ke, one[0, :h]), (v8, ve, one[0, h:])):
+        x = x.double().cpu()
+        e = torch.tensor([K8.exponent(float(m)) for m in x.abs().amax(-1)], dtype=torch.uint8)
+        want = K8.codes_of(K8.grid(x * torch.exp2(127 - e.double())[:, None])).view(torch.uint8).cuda()
+        assert (exps == e.cuda()).all() and (codes == want).all()
