@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // No faster: 64 rows a wave, one wave a SIMD (2.09 ms on a card where this took the same; ragged chunks
 // 380 us where this then took 290), half of the weights beside the values instead of the scores (the same).
 //
-// Over a cache in 8 bits (C = Cache8) the codes go the same way into a stage of their own (s_code) with the
+// Over a cache in 8 bits (C = Shared8) the codes go the same way into a stage of their own (s_code) with the
 // loads' order and addresses; behind a step's products each thread makes 16-bit
 // rows of the pieces that it brought itself, with the exponents of their blocks, in the places where the
 // products want them.  One prompt of 12,000 tokens (fp16) 1,331 us where 16-bit rows take 1,248, ragged chunks
