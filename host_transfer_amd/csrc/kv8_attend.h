@@ -6,7 +6,8 @@
 namespace ibp {
 namespace kv {
 
-// Workgroups of k_kv8_decode that a CU runs at a time, by its registers (columns of 16 rows).
+// Workgroups of k_kv8_decode that a CU runs at a time, by its registers (columns of 16 rows).  Measured with heads
+// of 128; those of up to 64 are run as these, though their registers leave room for five and three.
 constexpr uint32_t decode8_groups(uint32_t head_dim, uint32_t columns) {
   return head_dim <= 128 ? (columns == 1 ? 4 : 2) : (columns == 1 ? 2 : 1);
 }

@@ -254,7 +254,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   const uint32_t load_row = wave * RPL + lane / CH, place = lane % CH;
   const uint32_t lds_k = lds_address(s_k), lds_v = lds_address(s_v);
   // a load's rows lie in one page, at offsets that 32 bits hold
-  const bool same_page = cache.page.d % RPL == 0 && cache.token_stride <= (1u << 26);
+  const bool same_page = cache.page.d % (kEight ? RPL8 : RPL) == 0 && cache.token_stride <= (1u << 26);
   if (!kExact) {  // pieces past head_dim: never loaded, zeros
     if (kEight) {
 #pragma unroll
@@ -300,7 +300,7 @@ __global__ __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) void k_kv_chunk(
   auto bring8 = [&](const E* base, uint64_t at, uint64_t seen, bool is_k) {
     const uint32_t stage = lds_code + (is_k ? 0 : ST8 * kThreads * 16) + wave * (kWave * 16);
     const uint32_t first = wave * RPL8 + lane / CH8, c = lane % CH8 * 16;
-    if (seen == ~0ull && cache.page.d % RPL8 == 0 && cache.token_stride <= (1u << 26)) {
+    if (seen == ~0ull && same_page) {
       const uint32_t off = (uint32_t)((lane / CH8) * cache.token_stride) + c;
 #pragma unroll
       for (int i = 0; i < ST8; ++i) {
